@@ -64,6 +64,10 @@ typedef enum {
 #define VT_DEV_BAD_SEL 4  /* n_sel or a sel entry out of range (vt_sparse_decode); unit skipped */
 #define VT_DEV_BAD_ORDER 8 /* an `order` entry outside [0, B); that request slot was skipped */
 #define VT_DEV_TIMEOUT 16  /* a wait for work published by another CTA gave up (never expected) */
+#define VT_DEV_BAD_START 32 /* q_start / group_start not 0 = s[0] <= s[1] <= ... within its bound */
+#define VT_DEV_NO_PAGE 64   /* too few free pages; the requests that found none were left out */
+#define VT_DEV_BAD_REF 128  /* a page of a freed request had no reference left */
+#define VT_DEV_BAD_REQ 256  /* a request index out of range, listed twice, or a child row in use */
 
 /*
  * Paged K/V layout ("vTensor" metadata, reduced to one descriptor).
@@ -294,6 +298,183 @@ vt_status vt_sparse_decode_fused_static(const vt_paged_kv* kv, const vt_decode_a
  * reused by every layer.  seq_lens, order: device int32 [B]; B <= 65536.
  */
 vt_status vt_plan_requests(const int32_t* seq_lens, int32_t batch, int32_t* order, void* stream);
+
+/*
+ * ---- attention over whole prompts --------------------------------------------------------
+ *
+ * Causal attention of many query tokens per request over the paged cache: whole prompts,
+ * chunks of prompts with a context already cached, or a few drafted tokens, in one packed
+ * batch.  Request b's query rows are q[q_start[b] .. q_start[b+1]); they are the LAST
+ * q_start[b+1] - q_start[b] of its seq_lens[b] tokens, whose K/V are already in the pool (as
+ * for the decode calls), so the row of the i-th of n query tokens sees the tokens
+ * 0 .. seq_lens[b] - n + i:
+ *   out[t, hq] = sum_j softmax_j(sm_scale q[t, hq] . K[j, hq/G]) V[j, hq/G],
+ *   lse[t, hq] = log sum_j exp(sm_scale q[t, hq] . K[j, hq/G]).
+ *   q           bf16, element (t, hq, d) at q[t*sq_t + hq*D + d]; sq_t a multiple of 8
+ *   num_tokens  T: rows of q, out and lse.  Rows at or behind q_start[B] are left as they were
+ *   q_start     int32 [B+1], 0 = q_start[0] <= q_start[1] <= ... <= q_start[B] <= T; otherwise
+ *               nothing is computed and VT_DEV_BAD_START is reported
+ *   page_table, pt_stride, seq_lens, status   as in vt_decode_args
+ *   sm_scale    > 0
+ * A request with no query tokens is skipped.  One with seq_lens[b] below its number of query
+ * tokens, or of more pages than pt_stride, gets zero rows with lse = -inf (VT_DEV_BAD_LEN).  A
+ * page id outside [0, num_pages) takes no part (VT_DEV_BAD_PAGE): the rows are the attention
+ * over the request's other pages, zero with lse = -inf where none is left.  Pool slots behind
+ * a request's last token are never used, whatever they hold; K and V of the tokens a request
+ * has must be finite.  Scores, softmax statistics and accumulators are fp32; the weights are
+ * rounded once to bf16 for their product with V.
+ * Head shapes: (64, 64) and (128, 128), Hq/Hkv <= 8.  Pool strides as everywhere, and not 0
+ * for a dimension of more than one entry.
+ */
+typedef struct {
+  int32_t batch;       /* B */
+  int32_t num_q_heads; /* Hq, a multiple of Hkv */
+  int64_t num_tokens;  /* T */
+  const void* q;
+  int64_t sq_t;
+  const int32_t* q_start;
+  const int32_t* page_table;
+  int64_t pt_stride;
+  const int32_t* seq_lens;
+  float sm_scale;
+  int32_t* status;
+} vt_prefill_args;
+
+/*
+ * out: bf16 [T, Hq, Dv] contiguous, 16-byte aligned; lse: fp32 [T, Hq] or NULL.  workspace:
+ * vt_prefill_workspace_size() bytes, 256-byte aligned, any contents; it holds nothing between
+ * calls, and calls that can overlap on the GPU need one each.
+ */
+vt_status vt_prefill(const vt_paged_kv* kv, const vt_prefill_args* a, void* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace vt_prefill needs for these shapes on the current device; 0 for arguments
+ * that vt_prefill rejects and for an empty batch. */
+size_t vt_prefill_workspace_size(const vt_paged_kv* kv, const vt_prefill_args* a);
+
+/*
+ * ---- decode attention for requests that share a prefix -----------------------------------
+ *
+ * One query token per request over ALL its pages (no selection), where the requests
+ * group_start[g] .. group_start[g+1]-1 have the same first prefix_pages[g] page-table entries
+ * (a shared system prompt or document, or samples of one prompt after vt_fork_requests).  A
+ * group's prefix is read and attended once for all its rows; each request's own pages follow,
+ * and the two softmaxes are joined.  Results are those of attention over each request's pages
+ * by itself, up to fp32 rounding.
+ *   q             bf16 [B, Hq, D], contiguous, as in vt_decode_args
+ *   group_start   int32 [num_groups+1], 0 = group_start[0] <= ... <= group_start[num_groups]
+ *                 <= B; otherwise nothing is computed (VT_DEV_BAD_START).  Rows of requests at
+ *                 or behind group_start[num_groups] are left as they were
+ *   prefix_pages  int32 [num_groups], whole pages, 0 <= prefix_pages[g] <= pt_stride (outside:
+ *                 VT_DEV_BAD_LEN and zero rows for the group); the entries are read from the
+ *                 row of the group's first request
+ *   seq_lens      all tokens of the request, the prefix among them, at least one and at least
+ *                 16 prefix_pages[g] (otherwise VT_DEV_BAD_LEN and zero rows, lse = -inf)
+ * Bad page ids, unused slots, precision, head shapes and strides as for vt_prefill.
+ */
+typedef struct {
+  int32_t batch;       /* B */
+  int32_t num_q_heads; /* Hq, a multiple of Hkv */
+  int32_t num_groups;
+  const void* q;
+  const int32_t* group_start;
+  const int32_t* prefix_pages;
+  const int32_t* page_table;
+  int64_t pt_stride;
+  const int32_t* seq_lens;
+  float sm_scale;
+  int32_t* status;
+} vt_shared_prefix_args;
+
+/* out: bf16 [B, Hq, Dv]; lse: fp32 [B, Hq] or NULL; workspace as for vt_prefill. */
+vt_status vt_shared_prefix_decode(const vt_paged_kv* kv, const vt_shared_prefix_args* a, void* out,
+                                  float* lse, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Bytes of workspace vt_shared_prefix_decode needs (0 as for vt_prefill_workspace_size). */
+size_t vt_shared_prefix_workspace_size(const vt_paged_kv* kv, const vt_shared_prefix_args* a);
+
+/*
+ * ---- pages of the cache ------------------------------------------------------------------
+ *
+ * The cache's books are three int32 device arrays of the caller: page_table [R, pt_stride],
+ * seq_lens [R] (0: the row holds no request) and refs [num_pages], the number of rows that
+ * use a page (0: free).  The calls below change the books, and the pools where pages are
+ * copied, on the device; nothing is read back.  Pages are always taken lowest free id first,
+ * in the order of the list, so results do not depend on timing.  Calls on the same books must
+ * be ordered (one stream, or events).  Lists are int32 device arrays; entries outside [0, R)
+ * are skipped (VT_DEV_BAD_REQ).  Page copies move the K rows, the V rows (unless v_pool ==
+ * k_pool) and, where a centroid cache is given, the centroid rows.  All head shapes that
+ * vt_build_centroids takes, the MLA latent form (one copy of the shared rows) among them.
+ */
+typedef struct {
+  int32_t rows; /* R */
+  int32_t* page_table;
+  int64_t pt_stride;
+  int32_t* seq_lens;
+  int32_t* refs;
+  int32_t* status;
+} vt_page_books;
+
+/*
+ * Pages dst[i] become copies of pages src[i], i < n.  src may repeat; no page may be listed
+ * twice in dst, or in both lists.  A pair with an id outside [0, num_pages) is skipped
+ * (VT_DEV_BAD_PAGE).  centroids: fp32 [P, Hkv, D] or NULL.
+ */
+vt_status vt_copy_pages(const vt_paged_kv* kv, const int32_t* src, const int32_t* dst, int32_t n,
+                        float* centroids, int32_t* status, void* stream);
+
+/*
+ * Row children[i] becomes a fork of row parents[i], i < n: it has the parent's length and shares
+ * its full pages (refs + 1); a partly filled last page is copied to a page of its own, so that
+ * both can grow.  A parent may be listed often; a child must hold no request (seq_lens 0) and
+ * be listed once: other entries, and an empty parent's, are left out with VT_DEV_BAD_REQ (a
+ * child listed twice takes its first entry), a parent of more pages than pt_stride with
+ * VT_DEV_BAD_LEN.  A bad page id in a parent's row goes into the child's as it is, or leaves
+ * the copy's contents open (VT_DEV_BAD_PAGE).  With f free pages, the entries that need a page
+ * get one while the count of such entries up to and including them is at most f; the others
+ * are left out with VT_DEV_NO_PAGE.  No centroid is copied: a page that is not
+ * full has none.  workspace: vt_page_workspace_size(num_pages, n) bytes, 256-byte aligned, any
+ * contents, nothing kept.
+ */
+vt_status vt_fork_requests(const vt_paged_kv* kv, const vt_page_books* books,
+                           const int32_t* parents, const int32_t* children, int32_t n,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Row requests[i] grows by tokens[i] >= 0 tokens (a new request from length 0), i < n; the pages
+ * that this takes are appended to its row, with one reference.  A growth that is negative or
+ * past 16 pt_stride tokens is left out (VT_DEV_BAD_LEN); a row listed twice grows by its first
+ * entry (VT_DEV_BAD_REQ).  With f free pages, an entry gets its pages if the pages that the
+ * entries up to and including it need are at most f; otherwise it is left as it was
+ * (VT_DEV_NO_PAGE).  An entry that needs no page is always served.
+ */
+vt_status vt_extend_requests(const vt_page_books* books, int64_t num_pages,
+                             const int32_t* requests, const int32_t* tokens, int32_t n,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rows requests[i] end, i < n: every page of the row loses a reference, seq_lens becomes 0; the
+ * table entries stay as they are.  A row listed twice, or empty, is freed once, or not.  A bad
+ * page id is skipped (VT_DEV_BAD_PAGE), a page without a reference keeps 0 (VT_DEV_BAD_REF); a
+ * row of more pages than pt_stride frees those of its entries (VT_DEV_BAD_LEN).
+ */
+vt_status vt_free_requests(const vt_page_books* books, int64_t num_pages, const int32_t* requests,
+                           int32_t n, void* stream);
+
+/*
+ * The used pages move to the front of the pools: with u pages in use, the k-th lowest used page
+ * with an id >= u moves to the k-th lowest free id < u.  Contents, centroid rows (fp32
+ * [P, Hkv, D] or NULL), refs and the live entries of page_table follow; n_used[0] = u.  Bad
+ * page ids in the table stay (VT_DEV_BAD_PAGE), and so do live entries whose page has no
+ * reference (VT_DEV_BAD_REF).  workspace: vt_page_workspace_size(num_pages, 0).
+ */
+vt_status vt_compact_pages(const vt_paged_kv* kv, const vt_page_books* books, float* centroids,
+                           int32_t* n_used, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Bytes of workspace of the page calls for a pool of num_pages pages and lists of n entries. */
+size_t vt_page_workspace_size(int64_t num_pages, int32_t n);
 
 /* Static name of a status code. */
 const char* vt_status_string(vt_status s);

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(HERE, "libvt.so")
 
 VT_OK, VT_ERR_INVALID_ARG, VT_ERR_UNSUPPORTED, VT_ERR_CUDA = 0, 1, 2, 3
 VT_DEV_BAD_PAGE, VT_DEV_BAD_LEN, VT_DEV_BAD_SEL, VT_DEV_BAD_ORDER, VT_DEV_TIMEOUT = 1, 2, 4, 8, 16
+VT_DEV_BAD_START, VT_DEV_NO_PAGE, VT_DEV_BAD_REF, VT_DEV_BAD_REQ = 32, 64, 128, 256
 PAGE_SIZE = 16
 
 
@@ -50,10 +51,42 @@ class DecodeArgs(ctypes.Structure):
     ]
 
 
+class PrefillArgs(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+        ("num_tokens", ctypes.c_int64), ("q", ctypes.c_void_p), ("sq_t", ctypes.c_int64),
+        ("q_start", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("pt_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p),
+        ("sm_scale", ctypes.c_float), ("status", ctypes.c_void_p),
+    ]
+
+
+class SharedPrefixArgs(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32), ("q", ctypes.c_void_p),
+        ("group_start", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("pt_stride", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p), ("sm_scale", ctypes.c_float),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class PageBooks(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("pt_stride", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
 EXPORTS = ("vt_build_centroids", "vt_select_pages", "vt_select_pages_approx",
            "vt_select_pages_ws", "vt_sparse_decode_ws",
            "vt_sparse_decode", "vt_sparse_decode_fused", "vt_sparse_decode_step",
            "vt_fused_workspace_size", "vt_sparse_decode_fused_static", "vt_plan_requests",
+           "vt_prefill", "vt_prefill_workspace_size", "vt_shared_prefix_decode",
+           "vt_shared_prefix_workspace_size", "vt_copy_pages", "vt_fork_requests",
+           "vt_extend_requests", "vt_free_requests", "vt_compact_pages",
+           "vt_page_workspace_size",
            "vt_status_string",
            "vt_last_error_detail", "vt_abi_version")
 
@@ -75,6 +108,8 @@ def load_library(path: str = LIB_PATH):
             lib = ctypes.CDLL(path)
             P, I32, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
             kv, args = ctypes.POINTER(PagedKV), ctypes.POINTER(DecodeArgs)
+            prefill, shared = ctypes.POINTER(PrefillArgs), ctypes.POINTER(SharedPrefixArgs)
+            books = ctypes.POINTER(PageBooks)
             sigs = {
                 "vt_build_centroids": [kv, P, I32, P, P, P],
                 "vt_select_pages": [kv, args, P, P, P],
@@ -86,6 +121,13 @@ def load_library(path: str = LIB_PATH):
                 "vt_sparse_decode_step": [kv, args, P, I32, P, P, P, P, P, P, ctypes.c_size_t, P],
                 "vt_sparse_decode_fused_static": [kv, args, P, P, P, P, P],
                 "vt_plan_requests": [P, I32, P, P],
+                "vt_prefill": [kv, prefill, P, P, P, ctypes.c_size_t, P],
+                "vt_shared_prefix_decode": [kv, shared, P, P, P, ctypes.c_size_t, P],
+                "vt_copy_pages": [kv, P, P, I32, P, P, P],
+                "vt_fork_requests": [kv, books, P, P, I32, P, ctypes.c_size_t, P],
+                "vt_extend_requests": [books, I64, P, P, I32, P, ctypes.c_size_t, P],
+                "vt_free_requests": [books, I64, P, I32, P],
+                "vt_compact_pages": [kv, books, P, P, P, ctypes.c_size_t, P],
             }
             for name, argtypes in sigs.items():
                 fn = getattr(lib, name)
@@ -93,6 +135,12 @@ def load_library(path: str = LIB_PATH):
                 fn.restype = ctypes.c_int
             lib.vt_fused_workspace_size.argtypes = [kv, args]
             lib.vt_fused_workspace_size.restype = ctypes.c_size_t
+            lib.vt_prefill_workspace_size.argtypes = [kv, prefill]
+            lib.vt_prefill_workspace_size.restype = ctypes.c_size_t
+            lib.vt_shared_prefix_workspace_size.argtypes = [kv, shared]
+            lib.vt_shared_prefix_workspace_size.restype = ctypes.c_size_t
+            lib.vt_page_workspace_size.argtypes = [I64, I32]
+            lib.vt_page_workspace_size.restype = ctypes.c_size_t
             lib.vt_status_string.argtypes = [ctypes.c_int]
             lib.vt_status_string.restype = ctypes.c_char_p
             lib.vt_last_error_detail.argtypes = []
@@ -381,6 +429,266 @@ def vt_plan_requests(seq_lens: torch.Tensor, order: Optional[torch.Tensor] = Non
                               _stream(seq_lens))
     _check(rc, "vt_plan_requests")
     return order
+
+
+def _same_device(first: torch.Tensor, where: str, *others: Optional[torch.Tensor]) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise VtError(VT_ERR_INVALID_ARG, where, "tensors on different devices")
+
+
+def _table(page_table: torch.Tensor) -> None:
+    _need(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise VtError(VT_ERR_INVALID_ARG, "page_table", "must be [B, max_pages] with unit inner stride")
+
+
+def _sized(t: torch.Tensor, name: str, shape: tuple) -> None:
+    if tuple(t.shape) != shape:
+        raise VtError(VT_ERR_INVALID_ARG, name, f"must be {list(shape)}, got {list(t.shape)}")
+
+
+def _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, status):
+    kv = paged_kv(k_pool, v_pool)
+    _need(q, "q", torch.bfloat16)
+    _table(page_table)
+    _need(seq_lens, "seq_lens", torch.int32, contiguous=True)
+    _need(q_start, "q_start", torch.int32, contiguous=True)
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(q, "vt_prefill", k_pool, v_pool, page_table, seq_lens, q_start, status)
+    B = page_table.shape[0]
+    if q.dim() != 3 or q.shape[2] != kv.head_dim:
+        raise VtError(VT_ERR_INVALID_ARG, "q", f"must be [T, Hq, {kv.head_dim}]")
+    T, hq, d = q.shape
+    if q.stride(2) != 1 or (hq > 1 and q.stride(1) != d):
+        raise VtError(VT_ERR_INVALID_ARG, "q", "a token's heads must be contiguous")
+    _sized(seq_lens, "seq_lens", (B,))
+    _sized(q_start, "q_start", (B + 1,))
+    a = PrefillArgs(B, hq, T, q.data_ptr(), q.stride(0) if T > 1 else hq * d, q_start.data_ptr(),
+                    page_table.data_ptr(), page_table.stride(0) if B > 1 else page_table.shape[1],
+                    seq_lens.data_ptr(), float(sm_scale), _ptr(status))
+    return kv, a
+
+
+def _attend_outputs(q, out, lse, want_lse):
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    _need(out, "out", torch.bfloat16, contiguous=True)
+    _sized(out, "out", tuple(q.shape))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, contiguous=True)
+        _sized(lse, "lse", tuple(q.shape[:2]))
+    _same_device(q, "out/lse", out, lse)
+    return out, lse
+
+
+def _workspace(need: int, workspace, device):
+    """The given workspace, or a new one of ``need`` bytes (any contents)."""
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _need(workspace, "workspace", torch.uint8, contiguous=True)
+    if workspace.device != device:
+        raise VtError(VT_ERR_INVALID_ARG, "workspace", "on another device")
+    return workspace
+
+
+def _device_call(fn, where: str, t: torch.Tensor, *args):
+    """fn(*args, stream) with t's device current (kernels run where their tensors are)."""
+    if torch.cuda.current_device() == t.get_device():
+        _check(fn(*args, _stream(t)), where)
+    else:
+        with torch.cuda.device(t.device):
+            _check(fn(*args, _stream(t)), where)
+
+
+def prefill_workspace(q, k_pool, v_pool, page_table, seq_lens, q_start) -> Optional[torch.Tensor]:
+    """A workspace for vt_prefill with these shapes (any contents; None when none is needed)."""
+    lib = load_library()
+    kv, a = _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, 1.0, None)
+    return _workspace(int(lib.vt_prefill_workspace_size(ctypes.byref(kv), ctypes.byref(a))), None,
+                      q.device)
+
+
+def vt_prefill(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, out=None, lse=None,
+               status=None, want_lse=True, workspace=None):
+    """Causal attention of packed prompts over the paged cache.  Returns (out, lse or None).
+
+    ``q`` [T, Hq, D] (a view with another token stride is taken as it is): request b's rows are
+    q_start[b] .. q_start[b+1], the last of its seq_lens[b] tokens.  Rows behind q_start[B] are
+    left as they were.  ``workspace``: from prefill_workspace(); allocated here when not given.
+    """
+    lib = load_library()
+    kv, a = _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, status)
+    out, lse = _attend_outputs(q, out, lse, want_lse)
+    need = int(lib.vt_prefill_workspace_size(ctypes.byref(kv), ctypes.byref(a)))
+    workspace = _workspace(need, workspace, q.device)
+    _device_call(lib.vt_prefill, "vt_prefill", q, ctypes.byref(kv), ctypes.byref(a),
+                 out.data_ptr(), _ptr(lse), _ptr(workspace),
+                 0 if workspace is None else workspace.numel())
+    return out, lse
+
+
+def _shared_args(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pages, sm_scale,
+                 status):
+    kv = paged_kv(k_pool, v_pool)
+    _need(q, "q", torch.bfloat16, contiguous=True)
+    _table(page_table)
+    _need(seq_lens, "seq_lens", torch.int32, contiguous=True)
+    _need(group_start, "group_start", torch.int32, contiguous=True)
+    _need(prefix_pages, "prefix_pages", torch.int32, contiguous=True)
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(q, "vt_shared_prefix_decode", k_pool, v_pool, page_table, seq_lens, group_start,
+                 prefix_pages, status)
+    B, groups = page_table.shape[0], prefix_pages.numel()
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != kv.head_dim:
+        raise VtError(VT_ERR_INVALID_ARG, "q", f"must be [{B}, Hq, {kv.head_dim}]")
+    _sized(seq_lens, "seq_lens", (B,))
+    _sized(group_start, "group_start", (groups + 1,))
+    _sized(prefix_pages, "prefix_pages", (groups,))
+    a = SharedPrefixArgs(B, q.shape[1], groups, q.data_ptr(), group_start.data_ptr(),
+                         prefix_pages.data_ptr(), page_table.data_ptr(),
+                         page_table.stride(0) if B > 1 else page_table.shape[1],
+                         seq_lens.data_ptr(), float(sm_scale), _ptr(status))
+    return kv, a
+
+
+def shared_prefix_workspace(q, k_pool, v_pool, page_table, seq_lens, group_start,
+                            prefix_pages) -> Optional[torch.Tensor]:
+    """A workspace for vt_shared_prefix_decode with these shapes (any contents)."""
+    lib = load_library()
+    kv, a = _shared_args(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pages, 1.0,
+                         None)
+    return _workspace(int(lib.vt_shared_prefix_workspace_size(ctypes.byref(kv), ctypes.byref(a))),
+                      None, q.device)
+
+
+def vt_shared_prefix_decode(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pages,
+                            sm_scale, out=None, lse=None, status=None, want_lse=True,
+                            workspace=None):
+    """Decode attention over all pages of each request, where the requests group_start[g] ..
+    group_start[g+1] share their first prefix_pages[g] pages, which are attended once for the
+    group.  Returns (out [B, Hq, D], lse [B, Hq] or None).
+
+    ``workspace``: from shared_prefix_workspace(); allocated here when not given.
+    """
+    lib = load_library()
+    kv, a = _shared_args(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pages,
+                         sm_scale, status)
+    out, lse = _attend_outputs(q, out, lse, want_lse)
+    need = int(lib.vt_shared_prefix_workspace_size(ctypes.byref(kv), ctypes.byref(a)))
+    workspace = _workspace(need, workspace, q.device)
+    _device_call(lib.vt_shared_prefix_decode, "vt_shared_prefix_decode", q, ctypes.byref(kv),
+                 ctypes.byref(a), out.data_ptr(), _ptr(lse), _ptr(workspace),
+                 0 if workspace is None else workspace.numel())
+    return out, lse
+
+
+def _books(page_table, seq_lens, refs, status, *lists) -> PageBooks:
+    _table(page_table)
+    _need(seq_lens, "seq_lens", torch.int32, contiguous=True)
+    _need(refs, "refs", torch.int32, contiguous=True)
+    _sized(seq_lens, "seq_lens", (page_table.shape[0],))
+    if status is not None:
+        _need(status, "status", torch.int32)
+    for t in lists:
+        _need(t, "list of requests", torch.int32, contiguous=True)
+        _sized(t, "list of requests", (lists[0].numel(),))
+    _same_device(page_table, "page books", seq_lens, refs, status, *lists)
+    R, width = page_table.shape
+    return PageBooks(R, page_table.data_ptr(), page_table.stride(0) if R > 1 else width,
+                     seq_lens.data_ptr(), refs.data_ptr(), _ptr(status))
+
+
+def _pool_pages(k_pool, v_pool, refs, centroids) -> PagedKV:
+    kv = paged_kv(k_pool, v_pool)
+    if v_pool.shape[:3] != k_pool.shape[:3]:
+        raise VtError(VT_ERR_INVALID_ARG, "pools", "K and V pools of different shapes")
+    if refs is not None:
+        _sized(refs, "refs", (k_pool.shape[0],))
+    if centroids is not None:
+        _need(centroids, "centroids", torch.float32, contiguous=True)
+        _sized(centroids, "centroids", (k_pool.shape[0], k_pool.shape[2], k_pool.shape[3]))
+    _same_device(k_pool, "pools", v_pool, refs, centroids)
+    return kv
+
+
+def vt_copy_pages(k_pool, v_pool, src, dst, centroids=None, status=None) -> None:
+    """Pages dst[i] become copies of pages src[i] (K, V and, where given, centroid rows); no page
+    may be listed twice in ``dst``, or in both lists.  One pool as both K and V is copied once."""
+    lib = load_library()
+    kv = _pool_pages(k_pool, v_pool, None, centroids)
+    for t, name in ((src, "src"), (dst, "dst")):
+        _need(t, name, torch.int32, contiguous=True)
+    _sized(dst, "dst", tuple(src.shape))
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(k_pool, "vt_copy_pages", src, dst, status)
+    _device_call(lib.vt_copy_pages, "vt_copy_pages", k_pool, ctypes.byref(kv), src.data_ptr(),
+                 dst.data_ptr(), src.numel(), _ptr(centroids), _ptr(status))
+
+
+def page_workspace(num_pages: int, n: int, device) -> torch.Tensor:
+    """A workspace for the page calls: a pool of num_pages pages, lists of up to n requests."""
+    return torch.empty(int(load_library().vt_page_workspace_size(int(num_pages), int(n))),
+                       dtype=torch.uint8, device=device)
+
+
+def vt_fork_requests(k_pool, v_pool, page_table, seq_lens, refs, parents, children, status=None,
+                     workspace=None) -> None:
+    """Rows children[i] become forks of rows parents[i]: full pages are shared, a partly filled
+    last page is copied to a page of its own (the lowest free ones, in list order)."""
+    lib = load_library()
+    kv = _pool_pages(k_pool, v_pool, refs, None)
+    books = _books(page_table, seq_lens, refs, status, parents, children)
+    _same_device(k_pool, "vt_fork_requests", page_table)
+    n = parents.numel()
+    workspace = _workspace(int(lib.vt_page_workspace_size(refs.numel(), n)), workspace, refs.device)
+    _device_call(lib.vt_fork_requests, "vt_fork_requests", refs, ctypes.byref(kv),
+                 ctypes.byref(books), parents.data_ptr(), children.data_ptr(), n,
+                 workspace.data_ptr(), workspace.numel())
+
+
+def vt_extend_requests(page_table, seq_lens, refs, requests, tokens, status=None,
+                       workspace=None) -> None:
+    """Rows requests[i] grow by tokens[i] tokens; the pages that takes are appended (the lowest
+    free ones, in list order).  A new request starts from a row of length 0."""
+    lib = load_library()
+    books = _books(page_table, seq_lens, refs, status, requests, tokens)
+    n = requests.numel()
+    workspace = _workspace(int(lib.vt_page_workspace_size(refs.numel(), n)), workspace, refs.device)
+    _device_call(lib.vt_extend_requests, "vt_extend_requests", refs, ctypes.byref(books),
+                 refs.numel(), requests.data_ptr(), tokens.data_ptr(), n,
+                 _ptr(workspace), 0 if workspace is None else workspace.numel())
+
+
+def vt_free_requests(page_table, seq_lens, refs, requests, status=None) -> None:
+    """Rows requests[i] end: their pages lose a reference, their lengths become 0."""
+    lib = load_library()
+    books = _books(page_table, seq_lens, refs, status, requests)
+    _device_call(lib.vt_free_requests, "vt_free_requests", refs, ctypes.byref(books), refs.numel(),
+                 requests.data_ptr(), requests.numel())
+
+
+def vt_compact_pages(k_pool, v_pool, page_table, seq_lens, refs, centroids=None, n_used=None,
+                     status=None, workspace=None) -> torch.Tensor:
+    """The used pages move to the front of the pools, tables and counts with them.  Returns
+    n_used, int32 [1] on the device: pages n_used and up are free."""
+    lib = load_library()
+    kv = _pool_pages(k_pool, v_pool, refs, centroids)
+    books = _books(page_table, seq_lens, refs, status)
+    _same_device(k_pool, "vt_compact_pages", page_table, n_used)
+    if n_used is None:
+        n_used = torch.empty(1, dtype=torch.int32, device=refs.device)
+    _need(n_used, "n_used", torch.int32)
+    workspace = _workspace(int(lib.vt_page_workspace_size(refs.numel(), 0)), workspace, refs.device)
+    _device_call(lib.vt_compact_pages, "vt_compact_pages", refs, ctypes.byref(kv),
+                 ctypes.byref(books), _ptr(centroids), n_used.data_ptr(), workspace.data_ptr(),
+                 workspace.numel())
+    return n_used
 
 
 class PreparedCall:

@@ -1,11 +1,14 @@
 // api.cu -- the C ABI of libvt (include/vt.h): host-side argument checks, kernel choice and
 // launch.  No allocation, no synchronisation: every call only enqueues work on `stream`.
 #include <cmath>
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <atomic>
 
+#include "attend_params.cuh"
 #include "decode_params.cuh"
+#include "pages.cuh"
 
 namespace vt {
 cudaError_t launch_build_centroids(const vt_paged_kv& kv, const int32_t* pages, int n_pages,
@@ -281,6 +284,184 @@ vt_status launch_query_side(const vt_paged_kv* kv, const vt_decode_args* a, int 
   return ok();
 }
 
+// ---- dense attention: prompts and shared prefixes --------------------------------------------
+
+vt_status check_workspace(const void* ws, size_t ws_bytes, size_t need) {
+  if (!ws || ws_bytes < need)
+    return fail(VT_ERR_INVALID_ARG, "workspace of %zu bytes needed, %zu given", need,
+                ws ? ws_bytes : (size_t)0);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(VT_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  return ok();
+}
+
+// What both dense attention calls ask of the pools, the heads and the page table.
+vt_status attend_common(const vt_paged_kv* kv, int batch, int Hq, const void* q, int64_t pt_stride,
+                        float sm_scale, AttendParams* p) {
+  Shape sh;
+  vt_status s = classify(kv, Hq, &sh);
+  if (s != VT_OK) return s;
+  if (sh.path != kPathGqa)
+    return fail(VT_ERR_UNSUPPORTED, "dense attention needs head shape (64, 64) or (128, 128)");
+  const int64_t ext[3] = {kv->num_pages, VT_PAGE_SIZE, kv->num_kv_heads};
+  const int64_t st[6] = {kv->sk_p, kv->sk_t, kv->sk_h, kv->sv_p, kv->sv_t, kv->sv_h};
+  for (int i = 0; i < 6; ++i) {
+    if (ext[i % 3] > 1 && st[i] == 0)
+      return fail(VT_ERR_UNSUPPORTED, "a pool stride of 0 over more than one entry");
+    if (ext[i % 3] > 1 && st[i] >= ((int64_t)1 << 39))
+      return fail(VT_ERR_UNSUPPORTED, "a pool stride of 2^40 bytes or more");
+  }
+  if (batch < 0) return fail(VT_ERR_INVALID_ARG, "batch < 0");
+  if (batch > 65536) return fail(VT_ERR_UNSUPPORTED, "batch > 65536");
+  if (pt_stride < 1 || pt_stride > VT_MAX_PAGES_PER_REQUEST)
+    return fail(VT_ERR_UNSUPPORTED, "pt_stride %lld outside [1, %d]", (long long)pt_stride,
+                VT_MAX_PAGES_PER_REQUEST);
+  if (!std::isfinite(sm_scale) || !(sm_scale > 0.0f))
+    return fail(VT_ERR_INVALID_ARG, "sm_scale must be positive and finite");
+  if (!aligned16(q)) return fail(VT_ERR_UNSUPPORTED, "q not 16-byte aligned");
+  *p = AttendParams{};
+  p->kv = *kv;
+  p->Hkv = kv->num_kv_heads;
+  p->G = sh.G;
+  p->D = sh.D;
+  p->B = batch;
+  p->q = static_cast<const __nv_bfloat16*>(q);
+  p->pt_stride = pt_stride;
+  p->qscale = sm_scale * kLog2e;
+  return ok();
+}
+
+vt_status prefill_params(const vt_paged_kv* kv, const vt_prefill_args* a, AttendParams* p) {
+  vt_status s = check_kv(kv);
+  if (s != VT_OK) return s;
+  if (!a) return fail(VT_ERR_INVALID_ARG, "args is NULL");
+  s = attend_common(kv, a->batch, a->num_q_heads, a->q, a->pt_stride, a->sm_scale, p);
+  if (s != VT_OK) return s;
+  if (a->num_tokens < 0) return fail(VT_ERR_INVALID_ARG, "num_tokens < 0");
+  if (a->num_tokens > ((int64_t)1 << 30)) return fail(VT_ERR_UNSUPPORTED, "num_tokens > 2^30");
+  const int64_t row = (int64_t)a->num_q_heads * kv->head_dim;
+  if (a->sq_t % 8 != 0 || a->sq_t < 0 || (a->num_tokens > 1 && a->sq_t < row))
+    return fail(VT_ERR_UNSUPPORTED, "sq_t must be a multiple of 8 and at least Hq * D");
+  if (a->num_tokens > 1 && a->sq_t >= ((int64_t)1 << 39))
+    return fail(VT_ERR_UNSUPPORTED, "sq_t of 2^40 bytes or more");
+  if (a->batch > 0 && a->num_tokens > 0 &&
+      (!a->q || !a->q_start || !a->page_table || !a->seq_lens))
+    return fail(VT_ERR_INVALID_ARG, "q/q_start/page_table/seq_lens is NULL");
+  p->T = a->num_tokens;
+  p->sq_t = a->num_tokens > 1 ? a->sq_t : row;
+  p->start = a->q_start;
+  p->page_table = a->page_table;
+  p->seq_lens = a->seq_lens;
+  p->status = a->status;
+  return ok();
+}
+
+vt_status shared_params(const vt_paged_kv* kv, const vt_shared_prefix_args* a, AttendParams* p) {
+  vt_status s = check_kv(kv);
+  if (s != VT_OK) return s;
+  if (!a) return fail(VT_ERR_INVALID_ARG, "args is NULL");
+  s = attend_common(kv, a->batch, a->num_q_heads, a->q, a->pt_stride, a->sm_scale, p);
+  if (s != VT_OK) return s;
+  if (a->num_groups < 0) return fail(VT_ERR_INVALID_ARG, "num_groups < 0");
+  if (a->num_groups > 65536) return fail(VT_ERR_UNSUPPORTED, "num_groups > 65536");
+  if (a->batch > 0 && a->num_groups > 0 &&
+      (!a->q || !a->group_start || !a->prefix_pages || !a->page_table || !a->seq_lens))
+    return fail(VT_ERR_INVALID_ARG,
+                "q/group_start/prefix_pages/page_table/seq_lens is NULL");
+  p->n_groups = a->num_groups;
+  p->T = a->num_groups > 0 ? a->batch : 0;
+  p->sq_t = (int64_t)a->num_q_heads * kv->head_dim;
+  p->start = a->group_start;
+  p->prefix_pages = a->prefix_pages;
+  p->page_table = a->page_table;
+  p->seq_lens = a->seq_lens;
+  p->status = a->status;
+  return ok();
+}
+
+vt_status run_attend(AttendParams& p, void* out, float* lse, void* ws, size_t ws_bytes,
+                     void* stream) {
+  if (p.B == 0 || p.T == 0) return ok();
+  if (!out) return fail(VT_ERR_INVALID_ARG, "out is NULL");
+  if (!aligned16(out)) return fail(VT_ERR_UNSUPPORTED, "out not 16-byte aligned");
+  const int sms = sm_count();
+  vt_status s = check_workspace(ws, ws_bytes, attend_workspace_bytes(p, sms));
+  if (s != VT_OK) return s;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  cudaError_t e = launch_attend(p, ws, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  return ok();
+}
+
+// ---- pages of the cache ------------------------------------------------------------------------
+
+struct PageWorkspace {
+  size_t head, list, total;  // offsets: compaction's words, then a list's three arrays
+};
+
+PageWorkspace page_workspace(int64_t num_pages, int32_t n) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  PageWorkspace w;
+  w.head = 256;
+  w.list = w.head + up((size_t)num_pages * 3 * 4);
+  w.total = w.list + up((size_t)n * 3 * 4);
+  return w;
+}
+
+vt_status check_books(const vt_page_books* b, int64_t num_pages) {
+  if (!b) return fail(VT_ERR_INVALID_ARG, "books is NULL");
+  if (num_pages < 1) return fail(VT_ERR_INVALID_ARG, "num_pages < 1");
+  if (num_pages > (int64_t)INT32_MAX) return fail(VT_ERR_UNSUPPORTED, "num_pages above 2^31-1");
+  if (b->rows < 0) return fail(VT_ERR_INVALID_ARG, "rows < 0");
+  if (b->pt_stride < 1 || b->pt_stride > VT_MAX_PAGES_PER_REQUEST)
+    return fail(VT_ERR_UNSUPPORTED, "pt_stride %lld outside [1, %d]", (long long)b->pt_stride,
+                VT_MAX_PAGES_PER_REQUEST);
+  if (!b->refs || (b->rows > 0 && (!b->page_table || !b->seq_lens)))
+    return fail(VT_ERR_INVALID_ARG, "page_table/seq_lens/refs is NULL");
+  return ok();
+}
+
+// The pools as byte-for-byte copies see them; *sides: 1 where V is the K rows.
+vt_status page_pools(const vt_paged_kv* kv, float* centroids, PagePools* p, int* sides) {
+  vt_status s = check_kv(kv);
+  if (s != VT_OK) return s;
+  if (kv->head_dim % 8 != 0 || kv->head_dim_v % 8 != 0)
+    return fail(VT_ERR_UNSUPPORTED, "head dims must be multiples of 8");
+  if (centroids && !aligned16(centroids))
+    return fail(VT_ERR_UNSUPPORTED, "centroids not 16-byte aligned");
+  auto view = [&](const void* base, int64_t sp, int64_t st, int64_t sh, int dim) {
+    return PoolView{const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>(base)), sp, st,
+                    sh, kv->num_kv_heads, dim};
+  };
+  p->k = view(kv->k_pool, kv->sk_p, kv->sk_t, kv->sk_h, kv->head_dim);
+  p->v = view(kv->v_pool, kv->sv_p, kv->sv_t, kv->sv_h, kv->head_dim_v);
+  p->num_pages = kv->num_pages;
+  p->centroids = centroids;
+  p->cent_row = (int64_t)kv->num_kv_heads * kv->head_dim;
+  *sides = kv->k_pool == kv->v_pool ? 1 : 2;
+  return ok();
+}
+
+PageListParams list_params(const vt_page_books* b, int64_t num_pages, const int32_t* sources,
+                           const int32_t* targets, int32_t n, void* ws) {
+  PageListParams p{};
+  p.rows = b->rows;
+  p.page_table = b->page_table;
+  p.pt_stride = b->pt_stride;
+  p.seq_lens = b->seq_lens;
+  p.refs = b->refs;
+  p.status = b->status;
+  p.num_pages = num_pages;
+  p.sources = sources;
+  p.targets = targets;
+  p.n = n;
+  p.len = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + page_workspace(num_pages, n).list);
+  p.need = p.len + n;
+  p.base = p.need + n;
+  return p;
+}
+
 // ---- the library-owned scratch of vt_sparse_decode_fused_static ----------------------------
 
 // One per device the module is loaded on, zero-filled by CUDA at load.  The persistent
@@ -429,6 +610,134 @@ vt_status vt_plan_requests(const int32_t* seq_lens, int32_t batch, int32_t* orde
   if (batch > 65536) return fail(VT_ERR_UNSUPPORTED, "batch > 65536");
   cudaError_t e = launch_plan(seq_lens, batch, order, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
+  return ok();
+}
+
+vt_status vt_prefill(const vt_paged_kv* kv, const vt_prefill_args* a, void* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  AttendParams p;
+  vt_status s = prefill_params(kv, a, &p);
+  if (s != VT_OK) return s;
+  return run_attend(p, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t vt_prefill_workspace_size(const vt_paged_kv* kv, const vt_prefill_args* a) {
+  AttendParams p;
+  if (prefill_params(kv, a, &p) != VT_OK || p.B == 0 || p.T == 0) return 0;
+  return attend_workspace_bytes(p, sm_count());
+}
+
+vt_status vt_shared_prefix_decode(const vt_paged_kv* kv, const vt_shared_prefix_args* a, void* out,
+                                  float* lse, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  AttendParams p;
+  vt_status s = shared_params(kv, a, &p);
+  if (s != VT_OK) return s;
+  return run_attend(p, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t vt_shared_prefix_workspace_size(const vt_paged_kv* kv, const vt_shared_prefix_args* a) {
+  AttendParams p;
+  if (shared_params(kv, a, &p) != VT_OK || p.B == 0 || p.T == 0) return 0;
+  return attend_workspace_bytes(p, sm_count());
+}
+
+vt_status vt_copy_pages(const vt_paged_kv* kv, const int32_t* src, const int32_t* dst, int32_t n,
+                        float* centroids, int32_t* status, void* stream) {
+  PagePools pools;
+  int sides;
+  vt_status s = page_pools(kv, centroids, &pools, &sides);
+  if (s != VT_OK) return s;
+  if (n < 0) return fail(VT_ERR_INVALID_ARG, "n < 0");
+  if (n == 0) return ok();
+  if (!src || !dst) return fail(VT_ERR_INVALID_ARG, "src/dst is NULL");
+  cudaError_t e = launch_copy_pages(pools, src, dst, n, sides, status,
+                                    static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "copy_pages launch");
+  return ok();
+}
+
+size_t vt_page_workspace_size(int64_t num_pages, int32_t n) {
+  if (num_pages < 1 || num_pages > (int64_t)INT32_MAX || n < 0) return 0;
+  return page_workspace(num_pages, n).total;
+}
+
+vt_status vt_fork_requests(const vt_paged_kv* kv, const vt_page_books* books,
+                           const int32_t* parents, const int32_t* children, int32_t n,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  PagePools pools;
+  int sides;
+  vt_status s = page_pools(kv, nullptr, &pools, &sides);
+  if (s != VT_OK) return s;
+  s = check_books(books, kv->num_pages);
+  if (s != VT_OK) return s;
+  if (n < 0) return fail(VT_ERR_INVALID_ARG, "n < 0");
+  if (n == 0) return ok();
+  if (!parents || !children) return fail(VT_ERR_INVALID_ARG, "parents/children is NULL");
+  s = check_workspace(workspace, workspace_bytes, page_workspace(kv->num_pages, n).total);
+  if (s != VT_OK) return s;
+  const PageListParams p = list_params(books, kv->num_pages, parents, children, n, workspace);
+  cudaError_t e = launch_fork(pools, p, sides, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fork_requests launch");
+  return ok();
+}
+
+vt_status vt_extend_requests(const vt_page_books* books, int64_t num_pages,
+                             const int32_t* requests, const int32_t* tokens, int32_t n,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  vt_status s = check_books(books, num_pages);
+  if (s != VT_OK) return s;
+  if (n < 0) return fail(VT_ERR_INVALID_ARG, "n < 0");
+  if (n == 0) return ok();
+  if (!requests || !tokens) return fail(VT_ERR_INVALID_ARG, "requests/tokens is NULL");
+  s = check_workspace(workspace, workspace_bytes, page_workspace(num_pages, n).total);
+  if (s != VT_OK) return s;
+  const PageListParams p = list_params(books, num_pages, tokens, requests, n, workspace);
+  cudaError_t e = launch_extend(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "extend_requests launch");
+  return ok();
+}
+
+vt_status vt_free_requests(const vt_page_books* books, int64_t num_pages, const int32_t* requests,
+                           int32_t n, void* stream) {
+  vt_status s = check_books(books, num_pages);
+  if (s != VT_OK) return s;
+  if (n < 0) return fail(VT_ERR_INVALID_ARG, "n < 0");
+  if (n == 0) return ok();
+  if (!requests) return fail(VT_ERR_INVALID_ARG, "requests is NULL");
+  cudaError_t e = launch_free(*books, num_pages, requests, n, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "free_requests launch");
+  return ok();
+}
+
+vt_status vt_compact_pages(const vt_paged_kv* kv, const vt_page_books* books, float* centroids,
+                           int32_t* n_used, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  PagePools pools;
+  int sides;
+  vt_status s = page_pools(kv, centroids, &pools, &sides);
+  if (s != VT_OK) return s;
+  s = check_books(books, kv->num_pages);
+  if (s != VT_OK) return s;
+  if (!n_used) return fail(VT_ERR_INVALID_ARG, "n_used is NULL");
+  const PageWorkspace w = page_workspace(kv->num_pages, 0);
+  s = check_workspace(workspace, workspace_bytes, w.total);
+  if (s != VT_OK) return s;
+  CompactParams p{};
+  p.rows = books->rows;
+  p.page_table = books->page_table;
+  p.pt_stride = books->pt_stride;
+  p.seq_lens = books->seq_lens;
+  p.refs = books->refs;
+  p.status = books->status;
+  p.num_pages = kv->num_pages;
+  p.n_used = n_used;
+  p.n_moves = static_cast<int32_t*>(workspace);
+  p.src = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + w.head);
+  p.dst = p.src + kv->num_pages;
+  p.move_of = p.dst + kv->num_pages;
+  cudaError_t e = launch_compact(pools, p, sides, sm_count(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "compact_pages launch");
   return ok();
 }
 
