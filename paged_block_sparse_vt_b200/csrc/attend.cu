@@ -1,125 +1,954 @@
-// attend.cu -- dense attention over the paged cache: packed causal prompts (vt_prefill) and
-// decode with shared prefixes (vt_shared_prefix_decode).
+// attend.cu -- dense attention over the paged cache on the fifth-generation tensor cores: packed
+// causal prompts (vt_prefill) and decode with shared prefixes (vt_shared_prefix_decode).
 //
-// One warp per (token, query head): the lanes split the head's dims, keys come one after the
-// other, and the softmax runs with a running maximum and sum in base 2.
+// Rows.  The G query heads of a KV head see the same keys, so the rows of a tile are (token,
+// head) pairs, token first: 128 rows hold 128/G tokens, and one token of a decode call fills G of
+// them.  An item is two row tiles (256 rows), or one where there are no more tokens, against its
+// keys in steps of 128 (eight pages).
+//
+// One step, for either row tile t, with everything fp32 but the operands of the products:
+//   S_t = Q_t K^T                (tcgen05, 128 x 128 in tensor memory)
+//   m   = max(m, max_j S_t[r, j]), l = l f + sum_j p_j, p_j = 2^(c S_t[r, j] - c m), c = scale log2 e
+//   P_t = bf16(p)                (over the columns of S_t)
+//   O_t = O_t f + P_t V          (tcgen05, P_t read from tensor memory)
+// A warpgroup has one tile, a thread one row, so no sum or maximum crosses lanes.  f = 1 unless
+// the maximum rose: O_t is rescaled only when it rose by more than 2^kLazy since the last time
+// (until then p <= 2^kLazy, which loses nothing in bf16 or in fp32).
+//
+// One warp loads: K and V tiles alternate in a ring of shared-memory stages, each of them 8
+// pages by TMA in 128-byte swizzled boxes of 16 tokens x 64 dims, straight from the pools through
+// the page table.  The page that holds a request's last token is loaded from a negative token
+// coordinate, so that its tokens stand at the END of its 16 rows and the hardware fills the rest
+// with zeros: whatever the pool holds behind a request's end never gets into a product (0 x NaN
+// would spoil the row).  One warp issues all products; they complete in the order of issue,
+// which is why S_t of the next step may overwrite P_t as soon as P_t V is issued.
+//
+// Work is cut into equal shares of the whole batch, across items where need be (attend_plan.cuh);
+// an item that falls into several shares leaves unnormalised partial rows with their m and l, and
+// a second launch joins those: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+#include <cuda.h>
+
 #include "attend_params.cuh"
+#include "attend_plan.cuh"
 #include "common.cuh"
+#include "umma.cuh"
 
 namespace vt {
 
 namespace {
 
-// The page-table row, and the number of keys, of token t's query row; false: not computed.
-struct RowKeys {
-  const int32_t* table;    // its own row
-  const int32_t* shared;   // where the first `n_shared` entries are
-  int n_shared, keys;
-  bool ok, bad;
+constexpr int kThreads = 384;   // two softmax warpgroups, and one with the loading and product warps
+// Registers: a softmax thread holds its row of scores, 128 of them, beside the rest; what the
+// third warpgroup gives up goes to the other two (2 * 200 + 104 = 3 * 168, the launch's share).
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kDescs = 4;       // items described ahead
+constexpr int kBadRing = 16;    // key tiles whose page checks are kept (> tiles in flight)
+constexpr int kPlan = 1024;     // entries of the cost table in shared memory
+constexpr float kLazy = 8.0f;
+constexpr int kPagesTile = kKeys / kPage;
+
+template <int D>
+struct Cfg {
+  static constexpr int HALVES = D / 64;              // 64-dim boxes of a row
+  static constexpr int BOX = kKeys * 128;            // bytes of one half of a tile
+  static constexpr int TILE = HALVES * BOX;          // bytes of a Q, K or V tile
+  static constexpr int STAGES = D == 128 ? 4 : 8;
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE;
 };
 
-__device__ bool starts_ok(const int32_t* start, int n, int64_t bound) {
-  if (start[0] != 0) return false;
-  for (int i = 0; i < n; ++i)
-    if (start[i + 1] < start[i]) return false;
-  return start[n] <= bound;
+// What the loading warp tells the others about a piece of an item.
+struct Desc {
+  int tok0;            // first query token
+  int n_tok;           // tokens of the item; 0: no more items
+  int h;               // KV head
+  int j0, j1;          // key tiles [j0, j1)
+  int vis0, step;      // keys seen by token i of the item: vis0 + i step
+  int kv_len;          // valid keys
+  int slot;            // where a partial result goes: -1 none (write out), else see below
+  int whole;           // 1: all key tiles
+  int prefix;          // the item is a shared prefix
+};
+
+// A header of a partial slot.
+struct Head {
+  int tok0, n_tok, h, j0, j1, n_tiles, valid, pad;
+};
+
+struct Work {          // the workspace
+  Head* head;          // [2 ctas]
+  float* part;         // prompts: [2 ctas][256][D + 4]: slot 2c continues an item in CTA c, slot
+                       //   2c + 1 begins one; shared prefixes: [ctas][256][D + 4], slot c continues
+  float* first;        // shared prefixes: [2][B Hq][D + 4], the rows of items' first pieces:
+                       //   prefixes, then own pages
+  int64_t* line;       // shared prefixes: [units + 1] where each unit begins
+};
+
+// A partial row: O, then m (scaled, base 2) and l; padded to 16 bytes.
+template <int D>
+constexpr int kRowF = D + 4;
+
+struct Plan {
+  int64_t cost[kPlan + 1];
+};
+
+struct Shared {
+  Plan plan;
+  Desc desc[kDescs];
+  int bad[kBadRing];
+  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], desc_full[kDescs],
+      desc_empty[kDescs], kv_full[8], kv_empty[8], drain;
+  uint32_t tmem;
+  int abort;
+};
+
+// ---- the units ------------------------------------------------------------------------------
+
+template <bool SHARED>
+__device__ __forceinline__ int unit_count(const AttendParams& p) {
+  return SHARED ? p.n_groups + p.B : p.B;
 }
 
-__device__ RowKeys row_keys(const AttendParams& p, int64_t t) {
-  RowKeys r{};
-  const int n = p.prefix_pages ? p.n_groups : p.B;
-  if (t >= p.start[n]) return r;
-  int lo = 0, hi = n - 1;  // the last entry that starts at or before t
+// The group of request b, or -1: groups are few and their starts stay in L1.
+__device__ __forceinline__ int group_of(const AttendParams& p, int b) {
+  if (b >= p.start[p.n_groups]) return -1;
+  int lo = 0, hi = p.n_groups - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (p.start[mid] <= t) lo = mid; else hi = mid - 1;
+    if (p.start[mid] <= b) lo = mid; else hi = mid - 1;
   }
-  r.ok = true;
-  const int b = p.prefix_pages ? (int)t : lo;
-  const int len = p.seq_lens[b];
-  r.table = r.shared = p.page_table + (int64_t)b * p.pt_stride;
-  r.bad = len < 0 || len > p.pt_stride * kPage;
-  if (p.prefix_pages) {
-    r.shared = p.page_table + (int64_t)p.start[lo] * p.pt_stride;
-    r.n_shared = p.prefix_pages[lo];
-    r.bad |= r.n_shared < 0 || r.n_shared > p.pt_stride || len < 1 || len / kPage < r.n_shared;
-    r.keys = len;
+  return lo;
+}
+
+// Pages that a group shares as far as this call goes (a group of one shares with nobody); -1 bad.
+__device__ __forceinline__ int group_prefix(const AttendParams& p, int g) {
+  const int pages = p.prefix_pages[g];
+  if (pages < 0 || pages > p.pt_stride) return -1;
+  return p.start[g + 1] - p.start[g] >= 2 ? pages : 0;
+}
+
+template <bool SHARED>
+__device__ Unit load_unit(const AttendParams& p, int u) {
+  Unit x{};
+  if (!SHARED) {
+    const int len = p.seq_lens[u];
+    x.tok0 = p.start[u];
+    x.n = p.start[u + 1] - x.tok0;
+    x.row = u;
+    if (x.n == 0) return x;  // whatever its length
+    x.bad = len < x.n || len > p.pt_stride * kPage;
+    x.kv_len = x.bad ? 0 : len;
+    x.vis0 = x.bad ? 0 : len - x.n + 1;
+    x.step = x.bad ? 0 : 1;
+  } else if (u < p.n_groups) {
+    const int pages = group_prefix(p, u);
+    x.tok0 = x.row = p.start[u];
+    if (pages > 0) x.n = p.start[u + 1] - x.tok0;
+    x.kv_len = x.vis0 = max(pages, 0) * kPage;
   } else {
-    const int nq = p.start[lo + 1] - p.start[lo];
-    r.bad |= len < nq;
-    r.keys = len - nq + (int)(t - p.start[lo]) + 1;
+    const int b = u - p.n_groups, g = group_of(p, b);
+    x.tok0 = x.row = b;
+    if (g < 0) return x;
+    x.n = 1;
+    const int len = p.seq_lens[b], pages = group_prefix(p, g);
+    x.bad = pages < 0 || len < 1 || len > p.pt_stride * kPage ||
+            len < p.prefix_pages[g] * kPage;
+    x.page0 = max(pages, 0);
+    x.kv_len = x.vis0 = x.bad ? 0 : len - x.page0 * kPage;
   }
-  if (r.bad) r.keys = 0;
+  return x;
+}
+
+// ---- bounded waits --------------------------------------------------------------------------
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase, volatile int* abort_flag) {
+  for (int i = 0; i < 64; ++i)
+    if (umma::mbar_try_wait(bar, phase)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!umma::mbar_try_wait(bar, phase)) {
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > kWaitNs) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two floats rounded to a bf16 pair, `lo` in the low half
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) attend_rows_kernel(const AttendParams p) {
-  constexpr int E = D / 32;  // dims of a lane: lane * E ..
-  __shared__ int s_ok;
-  if (threadIdx.x == 0)
-    s_ok = starts_ok(p.start, p.prefix_pages ? p.n_groups : p.B, p.T);
-  __syncthreads();
-  if (!s_ok) {
-    if (threadIdx.x == 0) flag(p.status, VT_DEV_BAD_START);
-    return;
+// 32 bits, one for each key slot of a 32-wide column block that the row may use.
+struct RowMask {
+  int lim;            // slots below lim are visible ...
+  int hole0, hole1;   // ... but for these
+  uint32_t bad;       // pages of the tile that take no part, one bit each
+  __device__ __forceinline__ static uint32_t below(int n) {  // the n low bits
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
   }
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int Hq = p.Hkv * p.G;
-  const int64_t t = w / Hq;
-  if (t >= p.T) return;
-  const int hq = (int)(w - t * Hq), h = hq / p.G;
-  const RowKeys rk = row_keys(p, t);
-  if (!rk.ok) return;
-  if (rk.bad && lane == 0) flag(p.status, VT_DEV_BAD_LEN);
-  float q[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(p.q[t * p.sq_t + (int64_t)hq * D + lane * E + e]);
-    o[e] = 0.0f;
+  __device__ __forceinline__ uint32_t word(int w) const {
+    uint32_t m = below(lim - 32 * w);
+    m &= ~(below(hole1 - 32 * w) & ~below(hole0 - 32 * w));
+    if (bad >> (2 * w) & 1u) m &= 0xffff0000u;
+    if (bad >> (2 * w + 1) & 1u) m &= 0x0000ffffu;
+    return m;
   }
-  const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(p.kv.k_pool) + h * p.kv.sk_h;
-  const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(p.kv.v_pool) + h * p.kv.sv_h;
-  float m = -INFINITY, l = 0.0f;
-  for (int j = 0; j < rk.keys; ++j) {
-    const int page = (j / kPage < rk.n_shared ? rk.shared : rk.table)[j / kPage];
-    if (page < 0 || page >= p.kv.num_pages) {
-      if (lane == 0) flag(p.status, VT_DEV_BAD_PAGE);
-      j |= kPage - 1;
-      continue;
+};
+
+// ---- the kernel -----------------------------------------------------------------------------
+
+template <int N>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" : : "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_less() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" : : "n"(N));
+}
+
+template <int D, bool SHARED>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const AttendParams p, const Work w, const __grid_constant__ CUtensorMap q_map,
+                  const __grid_constant__ CUtensorMap q1_map,
+                  const __grid_constant__ CUtensorMap k_map,
+                  const __grid_constant__ CUtensorMap v_map) {
+  using C = Cfg<D>;
+  extern __shared__ unsigned char raw[];
+  __shared__ Shared sh;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t q_smem = base, kv_smem = base + 2 * C::TILE;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tpt = kTile / p.G;
+  const int cta = blockIdx.x;
+  volatile int* abort_flag = &sh.abort;
+
+  // The starts, then the cost of every unit, summed up over entries of `per` units each.
+  const int units = unit_count<SHARED>(p);
+  const int n_start = SHARED ? p.n_groups : p.B;
+  bool fine = true;
+  for (int i = threadIdx.x; i < n_start; i += kThreads)
+    fine &= p.start[i + 1] >= p.start[i] && (i > 0 || p.start[0] == 0);
+  fine &= p.start[n_start] <= p.T;
+  if (warp == kMmaWarp) umma::tmem_alloc(smem_u32(&sh.tmem), 512);
+  if (threadIdx.x == 0) {
+    sh.abort = 0;
+    umma::mbar_init(smem_u32(&sh.q_full), 1);
+    umma::mbar_init(smem_u32(&sh.q_empty), 1);
+    umma::mbar_init(smem_u32(&sh.drain), 1);
+    for (int t = 0; t < 2; ++t) {
+      umma::mbar_init(smem_u32(&sh.s_full[t]), 1);
+      umma::mbar_init(smem_u32(&sh.p_ready[t]), 4);
+      umma::mbar_init(smem_u32(&sh.o_full[t]), 1);
     }
-    const __nv_bfloat16* kr = kp + page * p.kv.sk_p + (j % kPage) * p.kv.sk_t + lane * E;
-    const __nv_bfloat16* vr = vp + page * p.kv.sv_p + (j % kPage) * p.kv.sv_t + lane * E;
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(kr[e]), s);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(kFull, s, x);
-    s *= p.qscale;
-    const float mn = fmaxf(m, s);
-    const float f = exp2f(m - mn), pr = exp2f(s - mn);
-    l = fmaf(l, f, pr);
-    m = mn;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(pr, __bfloat162float(vr[e]), o[e] * f);
+    for (int i = 0; i < kDescs; ++i) {
+      umma::mbar_init(smem_u32(&sh.desc_full[i]), 1);
+      umma::mbar_init(smem_u32(&sh.desc_empty[i]), 9);
+    }
+    for (int i = 0; i < C::STAGES; ++i) {
+      umma::mbar_init(smem_u32(&sh.kv_full[i]), 1);
+      umma::mbar_init(smem_u32(&sh.kv_empty[i]), 1);
+    }
+    umma::mbar_fence_init();
   }
-  const int64_t row = t * Hq + hq;
+  umma::fence_before_sync();
+  fine = __syncthreads_and(fine);
+  umma::fence_after_sync();
+  const uint32_t tm = sh.tmem;
+
+  const int per = (units + kPlan - 1) / kPlan, entries = (units + per - 1) / per;
+  if (fine)
+    for (int e = threadIdx.x; e < entries; e += kThreads) {
+      int64_t c = 0;
+      for (int u = e * per; u < min(units, (e + 1) * per); ++u) {
+        const Unit x = load_unit<SHARED>(p, u);
+        if (x.bad && cta == 0) flag(p.status, VT_DEV_BAD_LEN);
+        c += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
+      }
+      sh.plan.cost[e + 1] = c;
+    }
+  __syncthreads();
+  if (fine && warp == 0) {
+    const int run = (entries + 31) / 32;
+    int64_t sum = 0;
+    for (int e = lane * run; e < min(entries, (lane + 1) * run); ++e) sum += sh.plan.cost[e + 1];
+    int64_t before = sum;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    p.out[row * D + lane * E + e] = __float2bfloat16(l > 0.0f ? o[e] / l : 0.0f);
-  if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(kFull, before, o);
+      if (lane >= o) before += y;
+    }
+    before -= sum;
+    for (int e = lane * run; e < min(entries, (lane + 1) * run); ++e) {
+      const int64_t c = sh.plan.cost[e + 1];
+      sh.plan.cost[e + 1] = before + c;
+      before += c;
+    }
+    if (lane == 0) sh.plan.cost[0] = 0;
+  }
+  __syncthreads();
+  const int64_t total = fine ? sh.plan.cost[entries] : 0;
+  if (!fine && cta == 0 && threadIdx.x == 0) flag(p.status, VT_DEV_BAD_START);
+  const int n_cta = share_count(total, gridDim.x);
+
+  if (SHARED && cta == 0) {  // where the units begin, for the joining kernel; -1: nothing was done
+    if (fine) {
+      for (int e = threadIdx.x; e < entries; e += kThreads) {
+        int64_t c = sh.plan.cost[e];
+        for (int u = e * per; u < min(units, (e + 1) * per); ++u) {
+          const Unit x = load_unit<SHARED>(p, u);
+          w.line[u] = c;
+          c += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
+        }
+      }
+    }
+    if (threadIdx.x == 0) w.line[units] = fine ? total : -1;
+  }
+
+  const bool work = total > 0 && cta < n_cta;
+  if (warp >= kLoadWarp) {
+  regs_less<kRegsOther>();
+  if (warp == kLoadWarp) {
+    // ---- loading -----------------------------------------------------------------------------
+    if (lane == 0 && !SHARED) {
+      w.head[2 * cta].valid = 0;
+      w.head[2 * cta + 1].valid = 0;
+    }
+    int n_desc = 0, n_item = 0, n_tile = 0;
+    uint32_t filled = 0;  // stage uses, for the drain behind an abort
+    bool go = true;
+    if (work) {
+      const int64_t x0 = share_begin(total, n_cta, cta), x1 = share_begin(total, n_cta, cta + 1);
+      int lo = 0, hi = entries - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (sh.plan.cost[mid] <= x0) lo = mid; else hi = mid - 1;
+      }
+      int u = lo * per;
+      int64_t pos = sh.plan.cost[lo];
+      Unit un = load_unit<SHARED>(p, u);
+      int items = unit_items(un, tpt);
+      int64_t head_cost = cost_before(un, tpt, items);
+      while (pos + p.Hkv * head_cost <= x0) {  // x0 < total, so this ends at a unit with items
+        pos += p.Hkv * head_cost;
+        un = load_unit<SHARED>(p, ++u);
+        items = unit_items(un, tpt);
+        head_cost = cost_before(un, tpt, items);
+      }
+      int h = (int)((x0 - pos) / head_cost);
+      pos += h * head_cost;
+      int t = 0;
+      {
+        int a = 0, b = items - 1;
+        while (a < b) {
+          const int mid = (a + b + 1) >> 1;
+          if (cost_before(un, tpt, mid) <= x0 - pos) a = mid; else b = mid - 1;
+        }
+        t = a;
+        pos += cost_before(un, tpt, t);
+      }
+      while (go && pos < x1) {
+        const int64_t cost = item_cost(un, tpt, t);
+        const int keys = item_keys(un, tpt, t), wt = item_weight(un, tpt, t);
+        const int tiles = (keys + kKeys - 1) / kKeys;
+        const int j0 = cut_tile(x0 - pos, cost, wt, tiles), j1 = cut_tile(x1 - pos, cost, wt, tiles);
+        if (j0 < j1 || (tiles == 0 && pos >= x0)) {
+          // describe it
+          const int di = n_desc % kDescs;
+          go = wait(smem_u32(&sh.desc_empty[di]), ((n_desc / kDescs) & 1) ^ 1, abort_flag);
+          if (!go) break;
+          const int first = t * 2 * tpt, n_tok = min(un.n - first, 2 * tpt);
+          const bool whole = j0 == 0 && j1 == tiles;
+          const bool prefix = SHARED && u < p.n_groups;
+          if (lane == 0) {
+            Desc d;
+            d.tok0 = un.tok0 + first;
+            d.n_tok = n_tok;
+            d.h = h;
+            d.j0 = j0;
+            d.j1 = j1;
+            d.vis0 = un.vis0 + first * un.step;
+            d.step = un.step;
+            d.kv_len = un.kv_len;
+            d.whole = whole;
+            d.prefix = prefix;
+            d.slot = SHARED ? cta : whole ? -1 : 2 * cta + (j0 == 0);
+            sh.desc[di] = d;
+            if (!SHARED && !whole) {
+              Head hd{un.tok0 + first, n_tok, h, j0, j1, tiles, 1, 0};
+              w.head[d.slot] = hd;
+            }
+            umma::mbar_arrive(smem_u32(&sh.desc_full[di]));
+          }
+          ++n_desc;
+          // its tiles
+          const int n_pages = (un.kv_len + kPage - 1) / kPage;
+          const int last = un.kv_len - kPage * (n_pages - 1);  // tokens on the last page
+          const int32_t* table = p.page_table + (int64_t)un.row * p.pt_stride + un.page0;
+          auto page_id = [&](int j) {  // of lane's page among the four tiles from j
+            const int i = j * kPagesTile + lane;
+            return i < n_pages && j < j1 ? table[i] : -1;
+          };
+          int ids = 0, next = j0 < j1 ? page_id(j0) : 0;
+          for (int j = j0; go && j < j1; ++j, ++n_tile) {
+            if ((j - j0) % 4 == 0) {
+              ids = next;
+              next = page_id(j + 4);
+            }
+            const int mine = ((j - j0) & 3) * kPagesTile + (lane & 7);
+            int id = __shfl_sync(kFull, ids, mine);
+            const int i = j * kPagesTile + (lane & 7);
+            const bool there = i < n_pages;
+            const bool bad = there && (id < 0 || id >= p.kv.num_pages);
+            const uint32_t bads = __ballot_sync(kFull, bad) & 0xffu;
+            // tokens [0, 16), the last page's from a negative one; [16, 32): all zeros
+            int c_tok = i == n_pages - 1 ? last - kPage : 0;
+            if (!there || bad) {
+              id = 0;
+              c_tok = kPage;
+            }
+            if (lane == 0) {
+              sh.bad[n_tile % kBadRing] = (int)bads;
+              if (bads) flag(p.status, VT_DEV_BAD_PAGE);
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              const int use = 2 * n_tile + kv, st = use % C::STAGES;
+              const uint32_t full = smem_u32(&sh.kv_full[st]);
+              go = go && wait(smem_u32(&sh.kv_empty[st]), ((use / C::STAGES) & 1) ^ 1, abort_flag);
+              if (!go) break;
+              if (lane == 0) umma::mbar_expect_tx(full, C::TILE);
+              __syncwarp();
+              if (lane < kPagesTile * C::HALVES) {
+                const int half = lane / kPagesTile;
+                umma::tma_load_4d(kv_smem + st * C::TILE + half * C::BOX +
+                                      (lane & 7) * (kPage * 128),
+                                  kv ? &v_map : &k_map, half * 64, c_tok, h, id, full);
+              }
+              ++filled;
+              if (kv == 0 && j == j0) {
+                // q goes behind the first K tile: its buffer is free only when the last item's
+                // scores are done
+                go = wait(smem_u32(&sh.q_empty), (n_item & 1) ^ 1, abort_flag);
+                if (!go) break;
+                const bool one = SHARED && !prefix;
+                const bool two = n_tok > tpt;
+                if (lane == 0) {
+                  const uint32_t bar = smem_u32(&sh.q_full);
+                  const int bytes = (one ? p.G : p.G * tpt) * 128 * C::HALVES * (two ? 2 : 1);
+                  umma::mbar_expect_tx(bar, bytes);
+                  for (int tt = 0; tt < (two ? 2 : 1); ++tt)
+                    for (int half = 0; half < C::HALVES; ++half)
+                      umma::tma_load_3d(q_smem + tt * C::TILE + half * C::BOX,
+                                        one ? &q1_map : &q_map, half * 64, h * p.G,
+                                        un.tok0 + first + tt * tpt, bar);
+                }
+                ++n_item;
+              }
+            }
+          }
+        }
+        // the next item
+        pos += cost;
+        if (++t == items) {
+          t = 0;
+          if (++h == p.Hkv) {
+            h = 0;
+            do {
+              if (++u == units) break;
+              un = load_unit<SHARED>(p, u);
+              items = unit_items(un, tpt);
+            } while (items == 0);
+            if (u == units) break;
+          }
+        }
+      }
+    }
+    if (go) {
+      const int di = n_desc % kDescs;
+      go = wait(smem_u32(&sh.desc_empty[di]), ((n_desc / kDescs) & 1) ^ 1, abort_flag);
+      if (go && lane == 0) {
+        sh.desc[di].n_tok = 0;
+        umma::mbar_arrive(smem_u32(&sh.desc_full[di]));
+      }
+    }
+    if (!go) {  // copies in flight must land before the shared memory goes away
+      for (uint32_t i = 0; i < min(filled, (uint32_t)C::STAGES); ++i) {
+        const uint32_t use = filled - 1 - i;
+        const unsigned long long t0 = global_ns();
+        while (!umma::mbar_try_wait(smem_u32(&sh.kv_full[use % C::STAGES]),
+                                    (use / C::STAGES) & 1) &&
+               global_ns() - t0 < kWaitNs) {
+        }
+      }
+      const unsigned long long t0 = global_ns();
+      while (n_item > 0 && !umma::mbar_try_wait(smem_u32(&sh.q_full), (n_item - 1) & 1) &&
+             global_ns() - t0 < kWaitNs) {
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- products ----------------------------------------------------------------------------
+    constexpr uint32_t kIdS = umma::idesc_bf16(kTile, kKeys, false, false);
+    constexpr uint32_t kIdO = umma::idesc_bf16(kTile, D, false, true);
+    int n_desc = 0, n_item = 0, n_tile = 0;
+    uint32_t p_phase[2] = {0, 0};
+    bool go = true;
+    auto scores = [&](int t, int st) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (k / 4) * C::BOX + (k % 4) * 32;
+        umma::mma_bf16(tm + t * kKeys,
+                       umma::sdesc_sw128(q_smem + t * C::TILE + off, 0, 1024),
+                       umma::sdesc_sw128(kv_smem + st * C::TILE + off, 0, 1024), kIdS, k > 0);
+      }
+      umma::commit(smem_u32(&sh.s_full[t]));
+    };
+    auto values = [&](int t, int st, bool more) {
+#pragma unroll
+      for (int k = 0; k < kKeys / 16; ++k)
+        umma::mma_bf16_ta(tm + 2 * kKeys + t * D, tm + t * kKeys + k * 8,
+                          umma::sdesc_sw128(kv_smem + st * C::TILE + k * 2048, C::BOX, 1024), kIdO,
+                          more || k > 0);
+    };
+    while (true) {
+      const int di = n_desc % kDescs;
+      go = wait(smem_u32(&sh.desc_full[di]), (n_desc / kDescs) & 1, abort_flag);
+      if (!go) break;
+      const int n_tok = sh.desc[di].n_tok, j0 = sh.desc[di].j0, j1 = sh.desc[di].j1;
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(smem_u32(&sh.desc_empty[di]));
+      ++n_desc;
+      if (n_tok == 0) break;
+      if (j0 == j1) continue;
+      const int nt = n_tok > tpt ? 2 : 1;
+      for (int j = j0; go && j <= j1; ++j) {
+        // step j: the values of tile j - 1, then the scores of tile j, row tile by row tile
+        const int kst = 2 * n_tile % C::STAGES, vst = (2 * n_tile - 1) % C::STAGES;
+        if (j == j0) go = wait(smem_u32(&sh.q_full), n_item & 1, abort_flag);
+        if (go && j < j1)
+          go = wait(smem_u32(&sh.kv_full[kst]), (2 * n_tile / C::STAGES) & 1, abort_flag);
+        if (go && j > j0)
+          go = wait(smem_u32(&sh.kv_full[vst]), ((2 * n_tile - 1) / C::STAGES) & 1, abort_flag);
+        for (int t = 0; go && t < nt; ++t) {
+          if (j > j0) {
+            go = wait(smem_u32(&sh.p_ready[t]), p_phase[t], abort_flag);
+            if (!go) break;
+            p_phase[t] ^= 1;
+            umma::fence_after_sync();
+            values(t, vst, j > j0 + 1);
+            if (j == j1) umma::commit(smem_u32(&sh.o_full[t]));
+          } else {
+            umma::fence_after_sync();
+          }
+          if (j < j1) scores(t, kst);
+        }
+        if (!go) break;
+        if (j > j0) umma::commit(smem_u32(&sh.kv_empty[vst]));
+        if (j < j1) {
+          umma::commit(smem_u32(&sh.kv_empty[kst]));
+          if (j == j1 - 1) umma::commit(smem_u32(&sh.q_empty));
+          ++n_tile;
+        }
+      }
+      if (!go) break;
+      ++n_item;
+    }
+    if (!go) {  // let what was issued finish
+      umma::commit(smem_u32(&sh.drain));
+      const unsigned long long t0 = global_ns();
+      while (!umma::mbar_try_wait(smem_u32(&sh.drain), 0) && global_ns() - t0 < kWaitNs) {
+      }
+    }
+  }
+  } else {
+    regs_more<kRegsSoftmax>();
+    // ---- softmax and results -----------------------------------------------------------------
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tm_row = tm + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
+    const uint32_t tm_s = tm_row + t * kKeys, tm_o = tm_row + 2 * kKeys + t * D;
+    const float c = p.qscale, lazy = kLazy / c;
+    const int Hq = p.Hkv * p.G;
+    const int tok_row = row / p.G, head_row = row - tok_row * p.G;
+    uint32_t s_phase = 0, o_phase = 0;
+    int n_tile = 0;
+    for (int n_desc = 0;; ++n_desc) {
+      const int di = n_desc % kDescs;
+      if (!wait(smem_u32(&sh.desc_full[di]), (n_desc / kDescs) & 1, abort_flag)) break;
+      const Desc d = sh.desc[di];
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(smem_u32(&sh.desc_empty[di]));
+      if (d.n_tok == 0) break;
+      const int n_tok = min(tpt, d.n_tok - t * tpt);
+      if (n_tok <= 0) {
+        n_tile += d.j1 - d.j0;
+        continue;
+      }
+      const bool active = (warp & 3) * 32 < n_tok * p.G;
+      const int tok = t * tpt + min(tok_row, n_tok - 1);
+      const int vis = d.vis0 + tok * d.step;
+      const int vis_warp = d.vis0 + (t * tpt + min((warp & 3) * 32 / p.G, n_tok - 1)) * d.step;
+      const int n_pages = (d.kv_len + kPage - 1) / kPage;
+      const int gap = n_pages * kPage - d.kv_len;   // zero rows ahead of the last page's tokens
+      float m = -INFINITY, l = 0.0f;
+      bool ok = true;
+      for (int j = d.j0; j < d.j1; ++j, ++n_tile) {
+        ok = wait(smem_u32(&sh.s_full[t]), s_phase, abort_flag);
+        if (!ok) break;
+        s_phase ^= 1;
+        if (active) {
+          umma::fence_after_sync();
+          uint32_t s[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) umma::tmem_ld32_async(tm_s + 32 * i, s[i]);
+          umma::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) umma::tmem_landed(s[i]);
+          const uint32_t bad = (uint32_t)*(volatile int*)&sh.bad[n_tile % kBadRing];
+          const int slot0 = j * kKeys;
+          if (slot0 + kKeys > vis_warp || bad) {
+            RowMask rm;
+            const int last0 = (n_pages - 1) * kPage;  // the last page's first slot
+            rm.lim = (vis > last0 ? vis + gap : vis) - slot0;
+            rm.hole0 = last0 - slot0;
+            rm.hole1 = rm.hole0 + gap;
+            rm.bad = bad;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t ms = rm.word(i);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(ms >> e & 1u)) s[i][e] = __float_as_uint(-INFINITY);
+            }
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[i][e]));
+          if (__any_sync(kFull, mx > m + lazy || (m == -INFINITY && mx > m))) {
+            const float mn = fmaxf(m, mx);
+            const float f = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
+            m = mn;
+            l *= f;
+            if (j > d.j0) {
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) {
+                uint32_t o[32];
+                umma::tmem_ld32_async(tm_o + 32 * i, o);
+                umma::tmem_wait_ld();
+                umma::tmem_landed(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                umma::tmem_st32_async(tm_o + 32 * i, o);
+              }
+            }
+          }
+          const float mc = m == -INFINITY ? 0.0f : m * c;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float a = ex2(fmaf(__uint_as_float(s[2 * i + e / 16][2 * e % 32]), c, -mc));
+              const float b = ex2(fmaf(__uint_as_float(s[2 * i + e / 16][2 * e % 32 + 1]), c, -mc));
+              sum[e & 1] += a;
+              sum[2 + (e & 1)] += b;
+              pk[e] = pack2(a, b);
+            }
+            umma::tmem_st32_async(tm_s + 32 * i, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          umma::tmem_wait_st();
+          umma::fence_before_sync();
+        }
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(smem_u32(&sh.p_ready[t]));
+      }
+      if (!ok) break;
+      if (d.j0 < d.j1) {
+        if (!wait(smem_u32(&sh.o_full[t]), o_phase, abort_flag)) break;
+        o_phase ^= 1;
+        umma::fence_after_sync();
+      }
+      if (!active) continue;
+      const bool mine = row < n_tok * p.G;
+      const int64_t orow = (int64_t)(d.tok0 + tok) * Hq + d.h * p.G + head_row;
+      const float mc = m == -INFINITY ? -INFINITY : m * c;
+      if (!SHARED && d.whole) {
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          if (d.j0 < d.j1) {
+            umma::tmem_ld32_async(tm_o + 32 * i, o);
+            umma::tmem_wait_ld();
+            umma::tmem_landed(o);
+          }
+          if (mine) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 32 * i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (l > 0.0f) {
+                v.x = pack2(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
+                v.y = pack2(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
+                v.z = pack2(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
+                v.w = pack2(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
+              }
+              dst[e] = v;
+            }
+          }
+        }
+        if (mine && p.lse) p.lse[orow] = l > 0.0f ? mc * kLn2 + logf(l) : -INFINITY;
+      } else {
+        float* dst;
+        if (SHARED && d.j0 == 0)
+          dst = w.first + ((d.prefix ? 0 : (int64_t)p.B * Hq) + orow) * kRowF<D>;
+        else
+          dst = w.part + ((int64_t)d.slot * 2 * kTile + t * kTile + row) * kRowF<D>;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          if (d.j0 < d.j1) {
+            umma::tmem_ld32_async(tm_o + 32 * i, o);
+            umma::tmem_wait_ld();
+            umma::tmem_landed(o);
+          }
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4*>(dst)[8 * i + e] =
+                  l > 0.0f ? make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3])
+                           : make_uint4(0, 0, 0, 0);
+          }
+        }
+        if (mine) *reinterpret_cast<float2*>(dst + D) = make_float2(mc, l);
+      }
+    }
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (sh.abort && threadIdx.x == 0) flag(p.status, VT_DEV_TIMEOUT);
+  if (warp == kMmaWarp) umma::tmem_dealloc(tm, 512);
+}
+
+// ---- joining partial rows -------------------------------------------------------------------
+
+// A warp's running join of partial rows of D floats (lane: D/32 of them).
+template <int D>
+struct Join {
+  static constexpr int E = D / 32;
+  float o[E], m = -INFINITY, l = 0.0f;
+  __device__ __forceinline__ Join() {
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  }
+  __device__ __forceinline__ void add(const float* r, int lane) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(r + D));
+    float x[E];
+    if (E == 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(r) + lane);
+      x[0] = v.x; x[1] = v.y; x[E - 2] = v.z; x[E - 1] = v.w;
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(r) + lane);
+      x[0] = v.x; x[1] = v.y;
+    }
+    float M, fa, fb;
+    merge_scale(m, ml.x, M, fa, fb);
+    m = M;
+    l = l * fa + ml.y * fb;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * fa + x[e] * fb;
+  }
+  __device__ __forceinline__ void write(__nv_bfloat16* out, float* lse, int64_t row, int lane) {
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(out + row * D) + lane * (E / 2);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
+    if (lse && lane == 0) lse[row] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+  }
+};
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = kJoinThreads / 32;
+
+// Prompts: block (c, y) joins rows y * 8 .. of the item that begins in CTA c and ends in another.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_items_kernel(const AttendParams p, const Work w) {
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Head h0 = w.head[2 * c + 1];
+  if (!h0.valid) return;
+  const int tpt = kTile / p.G, Hq = p.Hkv * p.G;
+  const int r = blockIdx.y * kJoinRows + warp;  // row of the item
+  const int tile = r / kTile, in = r - tile * kTile;
+  const int tok = tile * tpt + in / p.G;
+  if (in >= tpt * p.G || tok >= h0.n_tok) return;
+  Join<D> a;
+  a.add(w.part + ((int64_t)(2 * c + 1) * 2 * kTile + r) * kRowF<D>, lane);
+  int done = h0.j1;
+  for (int k = c + 1; done < h0.n_tiles && k < (int)gridDim.x; ++k) {
+    const Head hk = w.head[2 * k];
+    if (!hk.valid) continue;  // its share lay within a key tile of another's
+    a.add(w.part + ((int64_t)2 * k * 2 * kTile + r) * kRowF<D>, lane);
+    done = hk.j1;
+  }
+  a.write(p.out, p.lse, (int64_t)(h0.tok0 + tok) * Hq + h0.h * p.G + in % p.G, lane);
+}
+
+// Shared prefixes: a warp joins one row: the pieces of its group's prefix, and of its own pages.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_rows_kernel(const AttendParams p, const Work w, int ctas) {
+  const int units = p.n_groups + p.B;
+  const int64_t total = w.line[units];
+  if (total < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int Hq = p.Hkv * p.G, tpt = kTile / p.G;
+  const int64_t orow = (int64_t)blockIdx.x * kJoinRows + warp;
+  if (orow >= (int64_t)p.B * Hq) return;
+  const int b = (int)(orow / Hq), hq = (int)(orow - (int64_t)b * Hq);
+  const int h = hq / p.G;
+  const int g = group_of(p, b);
+  if (g < 0) return;
+  const Unit own = load_unit<true>(p, p.n_groups + b);
+  Join<D> a;
+  const int n_cta = share_count(total, ctas);
+#pragma unroll 1
+  for (int part = 0; part < 2 && !own.bad; ++part) {
+    const int u = part ? p.n_groups + b : g;
+    const Unit un = part ? own : load_unit<true>(p, g);
+    if (un.n == 0) continue;
+    const int t = (b - un.tok0) / (2 * tpt), i = (b - un.tok0) - t * 2 * tpt;
+    const int r = i / tpt * kTile + i % tpt * p.G + (hq - h * p.G);  // the row within the item
+    const int64_t cost = item_cost(un, tpt, t);
+    const int64_t pos = w.line[u] + h * cost_before(un, tpt, unit_items(un, tpt)) +
+                        cost_before(un, tpt, t);
+    const int wt = item_weight(un, tpt, t);
+    const int tiles = (item_keys(un, tpt, t) + kKeys - 1) / kKeys;
+    if (tiles == 0) continue;
+    for (int c = share_of(total, n_cta, pos); c < n_cta; ++c) {
+      const int64_t x0 = share_begin(total, n_cta, c), x1 = share_begin(total, n_cta, c + 1);
+      if (x0 >= pos + cost) break;
+      const int j0 = cut_tile(x0 - pos, cost, wt, tiles), j1 = cut_tile(x1 - pos, cost, wt, tiles);
+      if (j0 >= j1) continue;
+      a.add(j0 == 0 ? w.first + ((part ? (int64_t)p.B * Hq : 0) + orow) * kRowF<D>
+                    : w.part + ((int64_t)c * 2 * kTile + r) * kRowF<D>,
+            lane);
+    }
+  }
+  a.write(p.out, p.lse, orow, lane);
+}
+
+// ---- host -----------------------------------------------------------------------------------
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Fills w from ws (NULL: only the size is wanted) and returns the bytes.
+size_t lay_out(const AttendParams& p, int ctas, void* ws, Work* w) {
+  const bool shared = p.prefix_pages != nullptr;
+  const size_t row = (size_t)(p.D + 4) * 4;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* r = ws ? static_cast<char*>(ws) + at : nullptr;
+    at += up256(bytes);
+    return r;
+  };
+  Work x{};
+  x.head = reinterpret_cast<Head*>(take(shared ? 0 : 2 * sizeof(Head) * ctas));
+  x.part = reinterpret_cast<float*>(take((size_t)(shared ? 1 : 2) * ctas * 2 * kTile * row));
+  x.first = reinterpret_cast<float*>(take(shared ? 2 * (size_t)p.B * p.Hkv * p.G * row : 0));
+  x.line = reinterpret_cast<int64_t*>(take(shared ? ((size_t)p.n_groups + p.B + 1) * 8 : 0));
+  if (w) *w = x;
+  return at;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// A bf16 tensor of `rank` dimensions (innermost 64-element boxes, 128-byte swizzle); strides in
+// elements, for dimensions 1 ..; what has one entry may have any stride.
+bool encode(CUtensorMap* m, const void* base, int rank, const int64_t* dims, const int64_t* strides,
+            const int* box) {
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    bx[i] = (cuuint32_t)box[i];
+    if (i) st[i - 1] = dims[i] > 1 ? (cuuint64_t)strides[i - 1] * 2 : 16;
+  }
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, bx,
+                     one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool SHARED>
+cudaError_t launch(const AttendParams& p, const Work& w, int ctas, cudaStream_t s) {
+  const int tpt = kTile / p.G;
+  CUtensorMap q, q1, k, v;
+  const int64_t qd[3] = {D, (int64_t)p.Hkv * p.G, p.T}, qs[2] = {D, p.sq_t};
+  const int qb[3] = {64, p.G, tpt}, qb1[3] = {64, p.G, 1};
+  const int64_t kd[4] = {D, kPage, p.Hkv, p.kv.num_pages};
+  const int64_t ks[3] = {p.kv.sk_t, p.kv.sk_h, p.kv.sk_p}, vs[3] = {p.kv.sv_t, p.kv.sv_h, p.kv.sv_p};
+  const int kb[4] = {64, kPage, 1, 1};
+  if (!encode_fn() || !encode(&q, p.q, 3, qd, qs, qb) || !encode(&q1, p.q, 3, qd, qs, qb1) ||
+      !encode(&k, p.kv.k_pool, 4, kd, ks, kb) || !encode(&v, p.kv.v_pool, 4, kd, vs, kb))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, SHARED>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  attend_kernel<D, SHARED><<<ctas, kThreads, Cfg<D>::SMEM, s>>>(p, w, q, q1, k, v);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (SHARED) {
+    const int64_t rows = (int64_t)p.B * p.Hkv * p.G;
+    join_rows_kernel<D><<<(unsigned)((rows + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, s>>>(
+        p, w, ctas);
+  } else {
+    join_items_kernel<D><<<dim3(ctas, 2 * kTile / kJoinRows), kJoinThreads, 0, s>>>(p, w);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t attend_workspace_bytes(const AttendParams&, int) { return 256; }
+size_t attend_workspace_bytes(const AttendParams& p, int sm_count) {
+  return lay_out(p, sm_count, nullptr, nullptr);
+}
 
-cudaError_t launch_attend(const AttendParams& p, void*, int, cudaStream_t s) {
-  const int64_t blocks = (p.T * p.Hkv * p.G + 7) / 8;
-  if (p.D == 128) attend_rows_kernel<128><<<(unsigned)blocks, 256, 0, s>>>(p);
-  else attend_rows_kernel<64><<<(unsigned)blocks, 256, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_attend(const AttendParams& p, void* ws, int sm_count, cudaStream_t s) {
+  Work w;
+  lay_out(p, sm_count, ws, &w);
+  const bool shared = p.prefix_pages != nullptr;
+  if (p.D == 128)
+    return shared ? launch<128, true>(p, w, sm_count, s) : launch<128, false>(p, w, sm_count, s);
+  return shared ? launch<64, true>(p, w, sm_count, s) : launch<64, false>(p, w, sm_count, s);
 }
 
 }  // namespace vt
