@@ -180,6 +180,25 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// two floats in one register pair, and the two-wide arithmetic on them
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // two floats rounded to a bf16 pair, `lo` in the low half
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
@@ -605,41 +624,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_phase ^= 1;
         if (active) {
           umma::fence_after_sync();
-          uint32_t s[4][32];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) umma::tmem_ld32_async(tm_s + 32 * i, s[i]);
-          umma::tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) umma::tmem_landed(s[i]);
           const uint32_t bad = (uint32_t)*(volatile int*)&sh.bad[n_tile % kBadRing];
           const int slot0 = j * kKeys;
-          if (slot0 + kKeys > vis_warp || bad) {
+          if (slot0 + kKeys > vis_warp || bad) {  // what a row may not see becomes -inf in place
             RowMask rm;
             const int last0 = (n_pages - 1) * kPage;  // the last page's first slot
             rm.lim = (vis > last0 ? vis + gap : vis) - slot0;
             rm.hole0 = last0 - slot0;
             rm.hole1 = rm.hole0 + gap;
             rm.bad = bad;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) {
+              uint32_t s[32];
+              umma::tmem_ld32_async(tm_s + 32 * i, s);
               const uint32_t ms = rm.word(i);
+              umma::tmem_wait_ld();
+              umma::tmem_landed(s);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(ms >> e & 1u)) s[i][e] = __float_as_uint(-INFINITY);
+                if (!(ms >> e & 1u)) s[e] = __float_as_uint(-INFINITY);
+              umma::tmem_st32_async(tm_s + 32 * i, s);
             }
+            umma::tmem_wait_st();
           }
-          float mx = -INFINITY;
+          // The scores are read twice, for the maximum and for the weights: a row of 128 does not
+          // stay in registers without spills, and a second read costs 32 cycles per 32 columns.
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i) {
+            uint32_t s0[32], s1[32];
+            umma::tmem_ld32_async(tm_s + 64 * i, s0);
+            umma::tmem_ld32_async(tm_s + 64 * i + 32, s1);
+            umma::tmem_wait_ld();
+            umma::tmem_landed(s0);
+            umma::tmem_landed(s1);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[i][e]));
-          if (__any_sync(kFull, mx > m + lazy || (m == -INFINITY && mx > m))) {
-            const float mn = fmaxf(m, mx);
+            for (int e = 0; e < 32; e += 4)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(s0[e + k]), __uint_as_float(s1[e + k])));
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          uint32_t s[2][32];
+          umma::tmem_ld32_async(tm_s, s[0]);
+          if (__any_sync(kFull, top > m + lazy || (m == -INFINITY && top > m))) {
+            const float mn = fmaxf(m, top);
             const float f = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
             m = mn;
             l *= f;
             if (j > d.j0) {
-#pragma unroll
+#pragma unroll 1
               for (int i = 0; i < D / 32; ++i) {
                 uint32_t o[32];
                 umma::tmem_ld32_async(tm_o + 32 * i, o);
@@ -652,21 +686,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float mc = m == -INFINITY ? 0.0f : m * c;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+          uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t pk[32];
+          for (int i = 0; i < 4; ++i) {
+            umma::tmem_wait_ld();
+            umma::tmem_landed(s[i & 1]);
+            // (P takes the columns of the scores already read)
+            if (i < 3) umma::tmem_ld32_async(tm_s + 32 * (i + 1), s[(i + 1) & 1]);
+            uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float a = ex2(fmaf(__uint_as_float(s[2 * i + e / 16][2 * e % 32]), c, -mc));
-              const float b = ex2(fmaf(__uint_as_float(s[2 * i + e / 16][2 * e % 32 + 1]), c, -mc));
-              sum[e & 1] += a;
-              sum[2 + (e & 1)] += b;
-              pk[e] = pack2(a, b);
+            for (int e = 0; e < 16; ++e) {
+              float x, y;
+              unpair(fma2(pair(__uint_as_float(s[i & 1][2 * e]), __uint_as_float(s[i & 1][2 * e + 1])),
+                          c2, mc2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              sum[e & 1] = add2(sum[e & 1], pair(x, y));
+              pk[e] = pack2(x, y);
             }
-            umma::tmem_st32_async(tm_s + 32 * i, pk);
+            umma::tmem_st16_async(tm_s + 16 * i, pk);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          {
+            float x0, y0, x1, y1;
+            unpair(sum[0], x0, y0);
+            unpair(sum[1], x1, y1);
+            l += (x0 + y0) + (x1 + y1);
+          }
           umma::tmem_wait_st();
           umma::fence_before_sync();
         }
