@@ -47,6 +47,8 @@ constexpr int kBadRing = 16;    // key tiles whose page checks are kept (> tiles
 constexpr int kPlan = 1024;     // entries of the cost table in shared memory
 constexpr float kLazy = 8.0f;
 constexpr int kPagesTile = kKeys / kPage;
+constexpr int kSoftWarps = 8;
+constexpr int kStage = 32 * 128;  // a softmax warp's staging: 128 bytes of each of its rows
 
 template <int D>
 struct Cfg {
@@ -54,7 +56,7 @@ struct Cfg {
   static constexpr int BOX = kKeys * 128;            // bytes of one half of a tile
   static constexpr int TILE = HALVES * BOX;          // bytes of a Q, K or V tile
   static constexpr int STAGES = D == 128 ? 4 : 8;
-  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE;
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + kSoftWarps * kStage;
 };
 
 // What the loading warp tells the others about a piece of an item.
@@ -88,15 +90,10 @@ struct Work {          // the workspace
 template <int D>
 constexpr int kRowF = D + 4;
 
-struct Plan {
-  int64_t cost[kPlan + 1];
-};
-
 struct Shared {
-  Plan plan;
   Desc desc[kDescs];
   int bad[kBadRing];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], desc_full[kDescs],
+  uint64_t q_full, q_empty, s_full[2], p_ready[2][2], o_full[2], desc_full[kDescs],
       desc_empty[kDescs], kv_full[8], kv_empty[8], drain;
   uint32_t tmem;
   int abort;
@@ -199,11 +196,45 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ float total2(uint64_t a, uint64_t b) {
+  float x0, y0, x1, y1;
+  unpair(a, x0, y0);
+  unpair(b, x1, y1);
+  return (x0 + y0) + (x1 + y1);
+}
+// 2^x of a pair on the special-function units
+__device__ __forceinline__ uint64_t exp2_unit(uint64_t x) {
+  float a, b;
+  unpair(x, a, b);
+  return pair(ex2(a), ex2(b));
+}
 // two floats rounded to a bf16 pair, `lo` in the low half
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+__device__ __forceinline__ uint32_t pack2(uint64_t p) {
+  float lo, hi;
+  unpair(p, lo, hi);
+  return pack2(lo, hi);
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
+                                            uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n"
+               :
+               : "r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
 }
 
 // 32 bits, one for each key slot of a 32-wide column block that the row may use.
@@ -249,6 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tpt = kTile / p.G;
   const int cta = blockIdx.x;
   volatile int* abort_flag = &sh.abort;
+  // the cost table lies where q comes later
+  int64_t* line = reinterpret_cast<int64_t*>(raw + (base - smem_u32(raw)));
 
   // The starts, then the cost of every unit, summed up over entries of `per` units each.
   const int units = unit_count<SHARED>(p);
@@ -265,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     umma::mbar_init(smem_u32(&sh.drain), 1);
     for (int t = 0; t < 2; ++t) {
       umma::mbar_init(smem_u32(&sh.s_full[t]), 1);
-      umma::mbar_init(smem_u32(&sh.p_ready[t]), 4);
+      umma::mbar_init(smem_u32(&sh.p_ready[t][0]), 4);
+      umma::mbar_init(smem_u32(&sh.p_ready[t][1]), 4);
       umma::mbar_init(smem_u32(&sh.o_full[t]), 1);
     }
     for (int i = 0; i < kDescs; ++i) {
@@ -292,13 +326,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x.bad && cta == 0) flag(p.status, VT_DEV_BAD_LEN);
         c += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
       }
-      sh.plan.cost[e + 1] = c;
+      line[e + 1] = c;
     }
   __syncthreads();
   if (fine && warp == 0) {
     const int run = (entries + 31) / 32;
     int64_t sum = 0;
-    for (int e = lane * run; e < min(entries, (lane + 1) * run); ++e) sum += sh.plan.cost[e + 1];
+    for (int e = lane * run; e < min(entries, (lane + 1) * run); ++e) sum += line[e + 1];
     int64_t before = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -307,21 +341,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     before -= sum;
     for (int e = lane * run; e < min(entries, (lane + 1) * run); ++e) {
-      const int64_t c = sh.plan.cost[e + 1];
-      sh.plan.cost[e + 1] = before + c;
+      const int64_t c = line[e + 1];
+      line[e + 1] = before + c;
       before += c;
     }
-    if (lane == 0) sh.plan.cost[0] = 0;
+    if (lane == 0) line[0] = 0;
   }
   __syncthreads();
-  const int64_t total = fine ? sh.plan.cost[entries] : 0;
+  const int64_t total = fine ? line[entries] : 0;
   if (!fine && cta == 0 && threadIdx.x == 0) flag(p.status, VT_DEV_BAD_START);
   const int n_cta = share_count(total, gridDim.x);
 
   if (SHARED && cta == 0) {  // where the units begin, for the joining kernel; -1: nothing was done
     if (fine) {
       for (int e = threadIdx.x; e < entries; e += kThreads) {
-        int64_t c = sh.plan.cost[e];
+        int64_t c = line[e];
         for (int u = e * per; u < min(units, (e + 1) * per); ++u) {
           const Unit x = load_unit<SHARED>(p, u);
           w.line[u] = c;
@@ -330,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (threadIdx.x == 0) w.line[units] = fine ? total : -1;
+    __syncthreads();  // (before q overwrites the table)
   }
 
   const bool work = total > 0 && cta < n_cta;
@@ -349,10 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int lo = 0, hi = entries - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (sh.plan.cost[mid] <= x0) lo = mid; else hi = mid - 1;
+        if (line[mid] <= x0) lo = mid; else hi = mid - 1;
       }
       int u = lo * per;
-      int64_t pos = sh.plan.cost[lo];
+      int64_t pos = line[lo];
       Unit un = load_unit<SHARED>(p, u);
       int items = unit_items(un, tpt);
       int64_t head_cost = cost_before(un, tpt, items);
@@ -374,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         t = a;
         pos += cost_before(un, tpt, t);
       }
+      umma::fence_async_smem();  // the table has been read
       while (go && pos < x1) {
         const int64_t cost = item_cost(un, tpt, t);
         const int keys = item_keys(un, tpt, t), wt = item_weight(un, tpt, t);
@@ -530,9 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       umma::commit(smem_u32(&sh.s_full[t]));
     };
-    auto values = [&](int t, int st, bool more) {
+    auto values = [&](int t, int st, int half, bool more) {
 #pragma unroll
-      for (int k = 0; k < kKeys / 16; ++k)
+      for (int k = half * (kKeys / 32); k < (half + 1) * (kKeys / 32); ++k)
         umma::mma_bf16_ta(tm + 2 * kKeys + t * D, tm + t * kKeys + k * 8,
                           umma::sdesc_sw128(kv_smem + st * C::TILE + k * 2048, C::BOX, 1024), kIdO,
                           more || k > 0);
@@ -558,11 +594,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           go = wait(smem_u32(&sh.kv_full[vst]), ((2 * n_tile - 1) / C::STAGES) & 1, abort_flag);
         for (int t = 0; go && t < nt; ++t) {
           if (j > j0) {
-            go = wait(smem_u32(&sh.p_ready[t]), p_phase[t], abort_flag);
+            go = wait(smem_u32(&sh.p_ready[t][0]), p_phase[t], abort_flag);
             if (!go) break;
-            p_phase[t] ^= 1;
             umma::fence_after_sync();
-            values(t, vst, j > j0 + 1);
+            values(t, vst, 0, j > j0 + 1);
+            go = wait(smem_u32(&sh.p_ready[t][1]), p_phase[t], abort_flag);
+            if (!go) break;
+            umma::fence_after_sync();
+            values(t, vst, 1, true);
+            p_phase[t] ^= 1;
             if (j == j1) umma::commit(smem_u32(&sh.o_full[t]));
           } else {
             umma::fence_after_sync();
@@ -626,7 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma::fence_after_sync();
           const uint32_t bad = (uint32_t)*(volatile int*)&sh.bad[n_tile % kBadRing];
           const int slot0 = j * kKeys;
-          if (slot0 + kKeys > vis_warp || bad) {  // what a row may not see becomes -inf in place
+          const bool masked = slot0 + kKeys > vis_warp || bad;
+          if (masked) {  // what a row may not see becomes -inf in place
             RowMask rm;
             const int last0 = (n_pages - 1) * kPage;  // the last page's first slot
             rm.lim = (vis > last0 ? vis + gap : vis) - slot0;
@@ -650,23 +691,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           // The scores are read twice, for the maximum and for the weights: a row of 128 does not
           // stay in registers without spills, and a second read costs 32 cycles per 32 columns.
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          {
+            uint32_t s[4][32];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t s0[32], s1[32];
-            umma::tmem_ld32_async(tm_s + 64 * i, s0);
-            umma::tmem_ld32_async(tm_s + 64 * i + 32, s1);
+            for (int i = 0; i < 4; ++i) umma::tmem_ld32_async(tm_s + 32 * i, s[i]);
             umma::tmem_wait_ld();
-            umma::tmem_landed(s0);
-            umma::tmem_landed(s1);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
+            for (int i = 0; i < 4; ++i) umma::tmem_landed(s[i]);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(s0[e + k]), __uint_as_float(s1[e + k])));
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(s[i][e + k]),
+                                             __uint_as_float(s[i][e + 4 + k])));
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           uint32_t s[2][32];
           umma::tmem_ld32_async(tm_s, s[0]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           if (__any_sync(kFull, top > m + lazy || (m == -INFINITY && top > m))) {
             const float mn = fmaxf(m, top);
             const float f = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
@@ -674,14 +717,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             l *= f;
             if (j > d.j0) {
 #pragma unroll 1
-              for (int i = 0; i < D / 32; ++i) {
-                uint32_t o[32];
-                umma::tmem_ld32_async(tm_o + 32 * i, o);
-                umma::tmem_wait_ld();
-                umma::tmem_landed(o);
+              for (int i = 0; i < D / 16; ++i) {
+                uint32_t o[16];
+                umma::tmem_ld16(tm_o + 16 * i, o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                umma::tmem_st32_async(tm_o + 32 * i, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                umma::tmem_st16_async(tm_o + 16 * i, o);
               }
             }
           }
@@ -692,32 +733,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i) {
             umma::tmem_wait_ld();
             umma::tmem_landed(s[i & 1]);
-            // (P takes the columns of the scores already read)
             if (i < 3) umma::tmem_ld32_async(tm_s + 32 * (i + 1), s[(i + 1) & 1]);
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float x, y;
-              unpair(fma2(pair(__uint_as_float(s[i & 1][2 * e]), __uint_as_float(s[i & 1][2 * e + 1])),
-                          c2, mc2), x, y);
-              x = ex2(x);
-              y = ex2(y);
-              sum[e & 1] = add2(sum[e & 1], pair(x, y));
-              pk[e] = pack2(x, y);
+              uint64_t x = fma2(pair(__uint_as_float(s[i & 1][2 * e]),
+                                     __uint_as_float(s[i & 1][2 * e + 1])),
+                                c2, mc2);
+              x = exp2_unit(x);
+              sum[e & 1] = add2(sum[e & 1], x);
+              pk[e] = pack2(x);
             }
-            umma::tmem_st16_async(tm_s + 16 * i, pk);
+            umma::tmem_st16_async(tm_s + 16 * i, pk);  // (over scores that were read)
+            if (i & 1) {  // half of the keys: the product with their values can start
+              umma::tmem_wait_st();
+              umma::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) umma::mbar_arrive(smem_u32(&sh.p_ready[t][i >> 1]));
+            }
           }
-          {
-            float x0, y0, x1, y1;
-            unpair(sum[0], x0, y0);
-            unpair(sum[1], x1, y1);
-            l += (x0 + y0) + (x1 + y1);
-          }
-          umma::tmem_wait_st();
-          umma::fence_before_sync();
+          l += total2(sum[0], sum[1]);
+        } else if (lane == 0) {
+          umma::mbar_arrive(smem_u32(&sh.p_ready[t][0]));
+          umma::mbar_arrive(smem_u32(&sh.p_ready[t][1]));
         }
-        __syncwarp();
-        if (lane == 0) umma::mbar_arrive(smem_u32(&sh.p_ready[t]));
       }
       if (!ok) break;
       if (d.j0 < d.j1) {
@@ -726,58 +765,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma::fence_after_sync();
       }
       if (!active) continue;
-      const bool mine = row < n_tok * p.G;
+      // Results leave through shared memory, 128 bytes of each row at a time (16-byte piece c of
+      // row r at c ^ (r % 8)), so that a store covers whole lines: straight from a thread's own
+      // row it would touch 32 of them.
+      const bool whole = !SHARED && d.whole;
       const int64_t orow = (int64_t)(d.tok0 + tok) * Hq + d.h * p.G + head_row;
       const float mc = m == -INFINITY ? -INFINITY : m * c;
-      if (!SHARED && d.whole) {
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const int rows = min(32, n_tok * p.G - (warp & 3) * 32);  // of this warp, the valid ones
+      // each lane's eight rows r0, r0 + 4, .. in the stores: byte offsets from the result's base
+      const int r0 = lane >> 3, piece = lane & 7;
+      unsigned char* base_out =
+          whole ? reinterpret_cast<unsigned char*>(p.out)
+                : reinterpret_cast<unsigned char*>(
+                      SHARED && d.j0 == 0
+                          ? w.first + (d.prefix ? 0 : (int64_t)p.B * Hq) * kRowF<D>
+                          : w.part + ((int64_t)d.slot * 2 * kTile + t * kTile) * kRowF<D>);
+      const int64_t row_at = whole ? orow * D * 2
+                             : (SHARED && d.j0 == 0 ? orow : (int64_t)row) * kRowF<D> * 4;
+      const uint32_t stage = kv_smem + C::STAGES * C::TILE + warp * kStage;
+      const int passes = whole ? D / 64 : D / 32;
+#pragma unroll 1
+      for (int i = 0; i < passes; ++i) {
+        uint32_t o[2][16];
+        if (d.j0 < d.j1) {
+          const uint32_t src = tm_o + (whole ? 64 : 32) * i;
+          umma::tmem_ld16_async(src, o[0]);
+          umma::tmem_ld16_async(src + 16, o[1]);
+          umma::tmem_wait_ld();
+          umma::tmem_landed(o[0]);
+          umma::tmem_landed(o[1]);
+        }
+        if (!(l > 0.0f)) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t o[32];
-          if (d.j0 < d.j1) {
-            umma::tmem_ld32_async(tm_o + 32 * i, o);
-            umma::tmem_wait_ld();
-            umma::tmem_landed(o);
-          }
-          if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 32 * i);
+          for (int e = 0; e < 32; ++e) o[e >> 4][e & 15] = 0u;
+        }
+        if (whole) {  // dims 64 i .. 64 i + 31, then the 32 behind them
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (l > 0.0f) {
-                v.x = pack2(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
-                v.y = pack2(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
-                v.z = pack2(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
-                v.w = pack2(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
+          for (int part = 0; part < 2; ++part) {
+            if (part) {
+              if (d.j0 < d.j1) {
+                umma::tmem_ld16_async(tm_o + 64 * i + 32, o[0]);
+                umma::tmem_ld16_async(tm_o + 64 * i + 48, o[1]);
+                umma::tmem_wait_ld();
+                umma::tmem_landed(o[0]);
+                umma::tmem_landed(o[1]);
               }
-              dst[e] = v;
+              if (!(l > 0.0f)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e >> 4][e & 15] = 0u;
+              }
+            }
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = pack2(__uint_as_float(o[q4 >> 1][8 * (q4 & 1) + 2 * e]) * inv,
+                             __uint_as_float(o[q4 >> 1][8 * (q4 & 1) + 2 * e + 1]) * inv);
+              st_shared16(stage + lane * 128 + (((4 * part + q4) ^ (lane & 7)) << 4), v[0], v[1],
+                          v[2], v[3]);
             }
           }
-        }
-        if (mine && p.lse) p.lse[orow] = l > 0.0f ? mc * kLn2 + logf(l) : -INFINITY;
-      } else {
-        float* dst;
-        if (SHARED && d.j0 == 0)
-          dst = w.first + ((d.prefix ? 0 : (int64_t)p.B * Hq) + orow) * kRowF<D>;
-        else
-          dst = w.part + ((int64_t)d.slot * 2 * kTile + t * kTile + row) * kRowF<D>;
+        } else {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t o[32];
-          if (d.j0 < d.j1) {
-            umma::tmem_ld32_async(tm_o + 32 * i, o);
-            umma::tmem_wait_ld();
-            umma::tmem_landed(o);
-          }
-          if (mine) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<uint4*>(dst)[8 * i + e] =
-                  l > 0.0f ? make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3])
-                           : make_uint4(0, 0, 0, 0);
-          }
+          for (int q8 = 0; q8 < 8; ++q8)
+            st_shared16(stage + lane * 128 + ((q8 ^ (lane & 7)) << 4),
+                        o[q8 >> 2][4 * (q8 & 3)], o[q8 >> 2][4 * (q8 & 3) + 1],
+                        o[q8 >> 2][4 * (q8 & 3) + 2], o[q8 >> 2][4 * (q8 & 3) + 3]);
         }
-        if (mine) *reinterpret_cast<float2*>(dst + D) = make_float2(mc, l);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + 4 * k;
+          const int64_t at = __shfl_sync(kFull, row_at, r);
+          const uint4 v = ld_shared16(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+          if (r < rows) *reinterpret_cast<uint4*>(base_out + at + 128 * i + 16 * piece) = v;
+        }
+        __syncwarp();
+      }
+      if (lane < rows) {
+        if (!whole)
+          *reinterpret_cast<float2*>(base_out + row_at + D * 4) = make_float2(mc, l);
+        else if (p.lse)
+          p.lse[orow] = l > 0.0f ? mc * kLn2 + logf(l) : -INFINITY;
       }
     }
   }
