@@ -42,12 +42,13 @@ constexpr int kThreads = 384;   // two softmax warpgroups, and one with the load
 // third warpgroup gives up goes to the other two (2 * 200 + 104 = 3 * 168, the launch's share).
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kDescs = 4;       // items described ahead
+constexpr int kDescs = 6;       // items described ahead
 constexpr int kBadRing = 16;    // key tiles whose page checks are kept (> tiles in flight)
 constexpr int kPlan = 1024;     // entries of the cost table in shared memory
 constexpr float kLazy = 8.0f;
 constexpr int kPagesTile = kKeys / kPage;
 constexpr int kSoftWarps = 8;
+constexpr int kSmall = 32;      // rows of a small item
 constexpr int kStage = 32 * 128;  // a softmax warp's staging: 128 bytes of each of its rows
 
 template <int D>
@@ -55,8 +56,17 @@ struct Cfg {
   static constexpr int HALVES = D / 64;              // 64-dim boxes of a row
   static constexpr int BOX = kKeys * 128;            // bytes of one half of a tile
   static constexpr int TILE = HALVES * BOX;          // bytes of a Q, K or V tile
+  // wide: two Q tiles, 128 KB of K and V, staging of all softmax warps
   static constexpr int STAGES = D == 128 ? 4 : 8;
-  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + kSoftWarps * kStage;
+  static constexpr int WIDE = 2 * TILE + kSoftWarps * kStage + STAGES * TILE;
+  // narrow: one Q tile, 192 KB of K and V.  Items of up to kSmall rows fill only the first of the
+  // four parts of that tile; the second stages their results.  (The product reads 128 rows of Q
+  // all the same; the others are what stands there, and nobody looks at their results.)  Larger
+  // ones stage theirs over their own Q, so the next Q waits for them.
+  static constexpr int Q_SMALL = kSmall * 128;  // bytes of one half
+  static constexpr int STAGES_NARROW = D == 128 ? 6 : 12;
+  static constexpr int NARROW = TILE + STAGES_NARROW * TILE;
+  static constexpr int SMEM = 1024 + (WIDE > NARROW ? WIDE : NARROW);
 };
 
 // What the loading warp tells the others about a piece of an item.
@@ -83,7 +93,8 @@ struct Work {          // the workspace
                        //   2c + 1 begins one; shared prefixes: [ctas][256][D + 4], slot c continues
   float* first;        // shared prefixes: [2][B Hq][D + 4], the rows of items' first pieces:
                        //   prefixes, then own pages
-  int64_t* line;       // shared prefixes: [units + 1] where each unit begins
+  int64_t* line;       // shared prefixes: [units + 2] where each unit begins in its line, and the
+                       //   lengths of the two lines
 };
 
 // A partial row: O, then m (scaled, base 2) and l; padded to 16 bytes.
@@ -94,7 +105,8 @@ struct Shared {
   Desc desc[kDescs];
   int bad[kBadRing];
   uint64_t q_full, q_empty, s_full[2], p_ready[2][2], o_full[2], desc_full[kDescs],
-      desc_empty[kDescs], kv_full[8], kv_empty[8], drain;
+      desc_empty[kDescs], kv_full[12], kv_empty[12], hand[4], back[4], out_done[2], drain;
+  float2 ml[kTile];  // m and l of the second warpgroup's rows, where it shares the first's
   uint32_t tmem;
   int abort;
 };
@@ -125,7 +137,7 @@ __device__ __forceinline__ int group_prefix(const AttendParams& p, int g) {
 }
 
 template <bool SHARED>
-__device__ Unit load_unit(const AttendParams& p, int u) {
+__device__ Unit load_unit_raw(const AttendParams& p, int u) {
   Unit x{};
   if (!SHARED) {
     const int len = p.seq_lens[u];
@@ -153,6 +165,13 @@ __device__ Unit load_unit(const AttendParams& p, int u) {
     x.page0 = max(pages, 0);
     x.kv_len = x.vis0 = x.bad ? 0 : len - x.page0 * kPage;
   }
+  return x;
+}
+
+template <bool SHARED>
+__device__ __forceinline__ Unit load_unit(const AttendParams& p, int u) {
+  Unit x = load_unit_raw<SHARED>(p, u);
+  x.narrow = x.n <= kTile / p.G;
   return x;
 }
 
@@ -275,13 +294,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char raw[];
   __shared__ Shared sh;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-  const uint32_t q_smem = base, kv_smem = base + 2 * C::TILE;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpt = kTile / p.G;
   const int cta = blockIdx.x;
   volatile int* abort_flag = &sh.abort;
-  // the cost table lies where q comes later
-  int64_t* line = reinterpret_cast<int64_t*>(raw + (base - smem_u32(raw)));
+  // the cost tables of both lines lie where q comes later
+  int64_t* table0 = reinterpret_cast<int64_t*>(raw + (base - smem_u32(raw)));
+  int64_t* table1 = table0 + kPlan + 1;
 
   // The starts, then the cost of every unit, summed up over entries of `per` units each.
   const int units = unit_count<SHARED>(p);
@@ -295,6 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh.abort = 0;
     umma::mbar_init(smem_u32(&sh.q_full), 1);
     umma::mbar_init(smem_u32(&sh.q_empty), 1);
+    umma::mbar_init(smem_u32(&sh.out_done[0]), 4);
+    umma::mbar_init(smem_u32(&sh.out_done[1]), 4);
     umma::mbar_init(smem_u32(&sh.drain), 1);
     for (int t = 0; t < 2; ++t) {
       umma::mbar_init(smem_u32(&sh.s_full[t]), 1);
@@ -302,11 +323,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma::mbar_init(smem_u32(&sh.p_ready[t][1]), 4);
       umma::mbar_init(smem_u32(&sh.o_full[t]), 1);
     }
+    for (int i = 0; i < 4; ++i) {
+      umma::mbar_init(smem_u32(&sh.hand[i]), 1);
+      umma::mbar_init(smem_u32(&sh.back[i]), 1);
+    }
     for (int i = 0; i < kDescs; ++i) {
       umma::mbar_init(smem_u32(&sh.desc_full[i]), 1);
       umma::mbar_init(smem_u32(&sh.desc_empty[i]), 9);
     }
-    for (int i = 0; i < C::STAGES; ++i) {
+    for (int i = 0; i < 12; ++i) {
       umma::mbar_init(smem_u32(&sh.kv_full[i]), 1);
       umma::mbar_init(smem_u32(&sh.kv_empty[i]), 1);
     }
@@ -320,16 +345,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (units + kPlan - 1) / kPlan, entries = (units + per - 1) / per;
   if (fine)
     for (int e = threadIdx.x; e < entries; e += kThreads) {
-      int64_t c = 0;
+      int64_t c[2] = {0, 0};
       for (int u = e * per; u < min(units, (e + 1) * per); ++u) {
         const Unit x = load_unit<SHARED>(p, u);
         if (x.bad && cta == 0) flag(p.status, VT_DEV_BAD_LEN);
-        c += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
+        c[x.narrow] += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
       }
-      line[e + 1] = c;
+      table0[e + 1] = c[0];
+      table1[e + 1] = c[1];
     }
   __syncthreads();
-  if (fine && warp == 0) {
+  if (fine && warp < 2) {
+    int64_t* line = warp ? table1 : table0;
     const int run = (entries + 31) / 32;
     int64_t sum = 0;
     for (int e = lane * run; e < min(entries, (lane + 1) * run); ++e) sum += line[e + 1];
@@ -348,26 +375,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) line[0] = 0;
   }
   __syncthreads();
-  const int64_t total = fine ? line[entries] : 0;
   if (!fine && cta == 0 && threadIdx.x == 0) flag(p.status, VT_DEV_BAD_START);
-  const int n_cta = share_count(total, gridDim.x);
+  const int64_t wide = fine ? table0[entries] : 0, thin = fine ? table1[entries] : 0;
+  // this CTA's line, its number there and how many share it
+  const int split = first_narrow(wide, thin, gridDim.x);
+  const bool narrow = cta >= split;
+  const int64_t* line = narrow ? table1 : table0;
+  const int64_t total = narrow ? thin : wide;
+  const int rank = narrow ? cta - split : cta;
+  const int n_cta = share_count(total, narrow ? gridDim.x - split : split);
 
   if (SHARED && cta == 0) {  // where the units begin, for the joining kernel; -1: nothing was done
     if (fine) {
       for (int e = threadIdx.x; e < entries; e += kThreads) {
-        int64_t c = line[e];
+        int64_t c[2] = {table0[e], table1[e]};
         for (int u = e * per; u < min(units, (e + 1) * per); ++u) {
           const Unit x = load_unit<SHARED>(p, u);
-          w.line[u] = c;
-          c += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
+          w.line[u] = c[x.narrow];
+          c[x.narrow] += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
         }
       }
     }
-    if (threadIdx.x == 0) w.line[units] = fine ? total : -1;
-    __syncthreads();  // (before q overwrites the table)
+    if (threadIdx.x == 0) {
+      w.line[units] = fine ? wide : -1;
+      w.line[units + 1] = thin;
+    }
+    __syncthreads();  // (before q overwrites the tables)
   }
 
-  const bool work = total > 0 && cta < n_cta;
+  // shared memory of the two kinds
+  const uint32_t q_smem = base;
+  const uint32_t kv_smem = base + (narrow ? C::TILE : 2 * C::TILE + kSoftWarps * kStage);
+  auto is_small = [&](int n_tok) { return narrow && n_tok * p.G <= kSmall; };
+  const int stages = narrow ? C::STAGES_NARROW : C::STAGES;
+
+  const bool work = total > 0 && rank < n_cta;
   if (warp >= kLoadWarp) {
   regs_less<kRegsOther>();
   if (warp == kLoadWarp) {
@@ -377,10 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.head[2 * cta + 1].valid = 0;
     }
     int n_desc = 0, n_item = 0, n_tile = 0;
-    uint32_t filled = 0;  // stage uses, for the drain behind an abort
+    int n_out = 0;        // items whose results are known to be out
+    bool small_before = true;
+    int st = 0;           // the ring's next stage and its phase
+    uint32_t ph = 0, filled = 0;
     bool go = true;
     if (work) {
-      const int64_t x0 = share_begin(total, n_cta, cta), x1 = share_begin(total, n_cta, cta + 1);
+      const int64_t x0 = share_begin(total, n_cta, rank), x1 = share_begin(total, n_cta, rank + 1);
       int lo = 0, hi = entries - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -389,12 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int u = lo * per;
       int64_t pos = line[lo];
       Unit un = load_unit<SHARED>(p, u);
-      int items = unit_items(un, tpt);
+      int items = un.narrow == narrow ? unit_items(un, tpt) : 0;
       int64_t head_cost = cost_before(un, tpt, items);
       while (pos + p.Hkv * head_cost <= x0) {  // x0 < total, so this ends at a unit with items
         pos += p.Hkv * head_cost;
         un = load_unit<SHARED>(p, ++u);
-        items = unit_items(un, tpt);
+        items = un.narrow == narrow ? unit_items(un, tpt) : 0;
         head_cost = cost_before(un, tpt, items);
       }
       int h = (int)((x0 - pos) / head_cost);
@@ -476,9 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
-              const int use = 2 * n_tile + kv, st = use % C::STAGES;
               const uint32_t full = smem_u32(&sh.kv_full[st]);
-              go = go && wait(smem_u32(&sh.kv_empty[st]), ((use / C::STAGES) & 1) ^ 1, abort_flag);
+              go = go && wait(smem_u32(&sh.kv_empty[st]), ph ^ 1, abort_flag);
               if (!go) break;
               if (lane == 0) umma::mbar_expect_tx(full, C::TILE);
               __syncwarp();
@@ -489,21 +533,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   kv ? &v_map : &k_map, half * 64, c_tok, h, id, full);
               }
               ++filled;
+              if (++st == stages) {
+                st = 0;
+                ph ^= 1;
+              }
               if (kv == 0 && j == j0) {
                 // q goes behind the first K tile: its buffer is free only when the last item's
                 // scores are done
                 go = wait(smem_u32(&sh.q_empty), (n_item & 1) ^ 1, abort_flag);
                 if (!go) break;
-                const bool one = SHARED && !prefix;
-                const bool two = n_tok > tpt;
+                const int tiles_q = n_tok > tpt ? 2 : 1;
+                const bool small = is_small(n_tok);
+                // results out: of the last item where the two meet in shared memory, else of the
+                // one before, so that no phase of the two barriers is passed unseen
+                const int outs = !narrow ? 0 : small && small_before ? n_item - 1 : n_item;
+                for (; go && n_out < outs; ++n_out)
+                  go = wait(smem_u32(&sh.out_done[n_out & 1]), n_out >> 1 & 1, abort_flag);
+                if (!go) break;
+                small_before = small;
                 if (lane == 0) {
                   const uint32_t bar = smem_u32(&sh.q_full);
-                  const int bytes = (one ? p.G : p.G * tpt) * 128 * C::HALVES * (two ? 2 : 1);
-                  umma::mbar_expect_tx(bar, bytes);
-                  for (int tt = 0; tt < (two ? 2 : 1); ++tt)
+                  const int box = p.G * (small ? kSmall / p.G : tpt) * 128;
+                  umma::mbar_expect_tx(bar, box * C::HALVES * tiles_q);
+                  for (int tt = 0; tt < tiles_q; ++tt)
                     for (int half = 0; half < C::HALVES; ++half)
-                      umma::tma_load_3d(q_smem + tt * C::TILE + half * C::BOX,
-                                        one ? &q1_map : &q_map, half * 64, h * p.G,
+                      umma::tma_load_3d(q_smem + tt * C::TILE + half * (small ? C::Q_SMALL : C::BOX),
+                                        small ? &q1_map : &q_map, half * 64, h * p.G,
                                         un.tok0 + first + tt * tpt, bar);
                 }
                 ++n_item;
@@ -520,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             do {
               if (++u == units) break;
               un = load_unit<SHARED>(p, u);
-              items = unit_items(un, tpt);
+              items = un.narrow == narrow ? unit_items(un, tpt) : 0;
             } while (items == 0);
             if (u == units) break;
           }
@@ -536,12 +591,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!go) {  // copies in flight must land before the shared memory goes away
-      for (uint32_t i = 0; i < min(filled, (uint32_t)C::STAGES); ++i) {
-        const uint32_t use = filled - 1 - i;
+      for (uint32_t i = 0; i < min(filled, (uint32_t)stages); ++i) {
+        if (st-- == 0) {
+          st = stages - 1;
+          ph ^= 1;
+        }
         const unsigned long long t0 = global_ns();
-        while (!umma::mbar_try_wait(smem_u32(&sh.kv_full[use % C::STAGES]),
-                                    (use / C::STAGES) & 1) &&
-               global_ns() - t0 < kWaitNs) {
+        while (!umma::mbar_try_wait(smem_u32(&sh.kv_full[st]), ph) && global_ns() - t0 < kWaitNs) {
         }
       }
       const unsigned long long t0 = global_ns();
@@ -553,16 +609,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- products ----------------------------------------------------------------------------
     constexpr uint32_t kIdS = umma::idesc_bf16(kTile, kKeys, false, false);
     constexpr uint32_t kIdO = umma::idesc_bf16(kTile, D, false, true);
-    int n_desc = 0, n_item = 0, n_tile = 0;
-    uint32_t p_phase[2] = {0, 0};
+    int n_desc = 0, n_item = 0;
+    int k_st = 0, v_st = 1;  // the ring's next K and V stage, and their phases
+    uint32_t k_ph = 0, v_ph = 0, p_phase[2] = {0, 0};
     bool go = true;
-    auto scores = [&](int t, int st) {
+    auto scores = [&](int t, int q_tile, uint32_t q_half, int st) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k / 4) * C::BOX + (k % 4) * 32;
-        umma::mma_bf16(tm + t * kKeys,
-                       umma::sdesc_sw128(q_smem + t * C::TILE + off, 0, 1024),
-                       umma::sdesc_sw128(kv_smem + st * C::TILE + off, 0, 1024), kIdS, k > 0);
+        const uint32_t at = (k % 4) * 32;
+        umma::mma_bf16(
+            tm + t * kKeys,
+            umma::sdesc_sw128(q_smem + q_tile * C::TILE + (k / 4) * q_half + at, 0, 1024),
+            umma::sdesc_sw128(kv_smem + st * C::TILE + (k / 4) * C::BOX + at, 0, 1024), kIdS,
+            k > 0);
       }
       umma::commit(smem_u32(&sh.s_full[t]));
     };
@@ -583,38 +642,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n_desc;
       if (n_tok == 0) break;
       if (j0 == j1) continue;
-      const int nt = n_tok > tpt ? 2 : 1;
-      for (int j = j0; go && j <= j1; ++j) {
-        // step j: the values of tile j - 1, then the scores of tile j, row tile by row tile
-        const int kst = 2 * n_tile % C::STAGES, vst = (2 * n_tile - 1) % C::STAGES;
-        if (j == j0) go = wait(smem_u32(&sh.q_full), n_item & 1, abort_flag);
-        if (go && j < j1)
-          go = wait(smem_u32(&sh.kv_full[kst]), (2 * n_tile / C::STAGES) & 1, abort_flag);
-        if (go && j > j0)
-          go = wait(smem_u32(&sh.kv_full[vst]), ((2 * n_tile - 1) / C::STAGES) & 1, abort_flag);
-        for (int t = 0; go && t < nt; ++t) {
-          if (j > j0) {
+      // Step k: the values of key tile k - lag, then the scores of key tile k.  Two row tiles take
+      // every key tile one after the other.  One row tile alone would leave the tensor cores
+      // idle while its softmax runs, so it takes key tiles in turn as two: even ones in S_0 and
+      // O_0, odd ones in S_1 and O_1, each with its own maxima and sums, joined at the end.
+      const bool two = n_tok > tpt;
+      const int n = j1 - j0, lag = two ? 1 : 2;
+      const uint32_t q_half = is_small(n_tok) ? C::Q_SMALL : C::BOX;
+      go = wait(smem_u32(&sh.q_full), n_item & 1, abort_flag);
+      for (int k = 0; go && k < n + lag; ++k) {
+        const bool has_k = k < n, has_v = k >= lag && k - lag < n;
+        if (has_k)
+          go = wait(smem_u32(&sh.kv_full[k_st]), k_ph, abort_flag);
+        if (go && has_v) go = wait(smem_u32(&sh.kv_full[v_st]), v_ph, abort_flag);
+        const int t0 = two ? 0 : k & 1, t1 = two ? 1 : t0;
+        for (int t = t0; go && t <= t1; ++t) {
+          if (has_v) {
             go = wait(smem_u32(&sh.p_ready[t][0]), p_phase[t], abort_flag);
             if (!go) break;
             umma::fence_after_sync();
-            values(t, vst, 0, j > j0 + 1);
+            values(t, v_st, 0, k >= 2 * lag);
             go = wait(smem_u32(&sh.p_ready[t][1]), p_phase[t], abort_flag);
             if (!go) break;
             umma::fence_after_sync();
-            values(t, vst, 1, true);
+            values(t, v_st, 1, true);
             p_phase[t] ^= 1;
-            if (j == j1) umma::commit(smem_u32(&sh.o_full[t]));
+            if (!has_k) umma::commit(smem_u32(&sh.o_full[t]));
           } else {
             umma::fence_after_sync();
           }
-          if (j < j1) scores(t, kst);
+          if (has_k) scores(t, two ? t : 0, q_half, k_st);
         }
         if (!go) break;
-        if (j > j0) umma::commit(smem_u32(&sh.kv_empty[vst]));
-        if (j < j1) {
-          umma::commit(smem_u32(&sh.kv_empty[kst]));
-          if (j == j1 - 1) umma::commit(smem_u32(&sh.q_empty));
-          ++n_tile;
+        if (has_v) {
+          umma::commit(smem_u32(&sh.kv_empty[v_st]));
+          if ((v_st += 2) >= stages) {
+            v_st = 1;
+            v_ph ^= 1;
+          }
+        }
+        if (has_k) {
+          umma::commit(smem_u32(&sh.kv_empty[k_st]));
+          if (k == n - 1) umma::commit(smem_u32(&sh.q_empty));
+          if ((k_st += 2) >= stages) {
+            k_st = 0;
+            k_ph ^= 1;
+          }
         }
       }
       if (!go) break;
@@ -636,8 +709,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.qscale, lazy = kLazy / c;
     const int Hq = p.Hkv * p.G;
     const int tok_row = row / p.G, head_row = row - tok_row * p.G;
-    uint32_t s_phase = 0, o_phase = 0;
-    int n_tile = 0;
+    uint32_t s_phase = 0, o_phase = 0, hand_phase = 0;
+    bool lent = false;  // O_1 is the first warpgroup's to read
+    int n_tile = 0, n_item = 0;
     for (int n_desc = 0;; ++n_desc) {
       const int di = n_desc % kDescs;
       if (!wait(smem_u32(&sh.desc_full[di]), (n_desc / kDescs) & 1, abort_flag)) break;
@@ -645,26 +719,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) umma::mbar_arrive(smem_u32(&sh.desc_empty[di]));
       if (d.n_tok == 0) break;
-      const int n_tok = min(tpt, d.n_tok - t * tpt);
-      if (n_tok <= 0) {
-        n_tile += d.j1 - d.j0;
-        continue;
-      }
-      const bool active = (warp & 3) * 32 < n_tok * p.G;
-      const int tok = t * tpt + min(tok_row, n_tok - 1);
+      const bool two = d.n_tok > tpt;
+      const int rt = two ? t : 0;  // row tile
+      const int n_tok = min(tpt, d.n_tok - rt * tpt);
+      const bool active = (warp & 3) * 32 < n_tok * p.G, mine = row < n_tok * p.G;
+      const int tok = rt * tpt + min(tok_row, n_tok - 1);
       const int vis = d.vis0 + tok * d.step;
-      const int vis_warp = d.vis0 + (t * tpt + min((warp & 3) * 32 / p.G, n_tok - 1)) * d.step;
+      const int vis_warp = d.vis0 + (rt * tpt + min((warp & 3) * 32 / p.G, n_tok - 1)) * d.step;
       const int n_pages = (d.kv_len + kPage - 1) / kPage;
       const int gap = n_pages * kPage - d.kv_len;   // zero rows ahead of the last page's tokens
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
-      for (int j = d.j0; j < d.j1; ++j, ++n_tile) {
+      const int begin = two ? d.j0 : d.j0 + t, stride = two ? 1 : 2;
+      for (int j = begin; j < d.j1; j += stride) {
         ok = wait(smem_u32(&sh.s_full[t]), s_phase, abort_flag);
         if (!ok) break;
         s_phase ^= 1;
         if (active) {
           umma::fence_after_sync();
-          const uint32_t bad = (uint32_t)*(volatile int*)&sh.bad[n_tile % kBadRing];
+          const uint32_t bad = (uint32_t)*(volatile int*)&sh.bad[(n_tile + j - d.j0) % kBadRing];
           const int slot0 = j * kKeys;
           const bool masked = slot0 + kKeys > vis_warp || bad;
           if (masked) {  // what a row may not see becomes -inf in place
@@ -710,12 +783,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t s[2][32];
           umma::tmem_ld32_async(tm_s, s[0]);
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (__any_sync(kFull, top > m + lazy || (m == -INFINITY && top > m))) {
+          if (__any_sync(kFull, mine && (top > m + lazy || (m == -INFINITY && top > m)))) {
             const float mn = fmaxf(m, top);
             const float f = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
             m = mn;
             l *= f;
-            if (j > d.j0) {
+            if (j > begin) {
 #pragma unroll 1
               for (int i = 0; i < D / 16; ++i) {
                 uint32_t o[16];
@@ -746,6 +819,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             umma::tmem_st16_async(tm_s + 16 * i, pk);  // (over scores that were read)
             if (i & 1) {  // half of the keys: the product with their values can start
+              if (lent) {
+                wait(smem_u32(&sh.back[warp & 3]), hand_phase, abort_flag);
+                hand_phase ^= 1;
+                lent = false;
+              }
               umma::tmem_wait_st();
               umma::fence_before_sync();
               __syncwarp();
@@ -753,18 +831,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           l += total2(sum[0], sum[1]);
-        } else if (lane == 0) {
-          umma::mbar_arrive(smem_u32(&sh.p_ready[t][0]));
-          umma::mbar_arrive(smem_u32(&sh.p_ready[t][1]));
+        } else {
+          if (lent) {
+            wait(smem_u32(&sh.back[warp & 3]), hand_phase, abort_flag);
+            hand_phase ^= 1;
+            lent = false;
+          }
+          if (lane == 0) {
+            umma::mbar_arrive(smem_u32(&sh.p_ready[t][0]));
+            umma::mbar_arrive(smem_u32(&sh.p_ready[t][1]));
+          }
         }
       }
       if (!ok) break;
-      if (d.j0 < d.j1) {
+      n_tile += d.j1 - d.j0;
+      n_item += d.j0 < d.j1;
+      if (begin < d.j1) {
         if (!wait(smem_u32(&sh.o_full[t]), o_phase, abort_flag)) break;
         o_phase ^= 1;
         umma::fence_after_sync();
       }
-      if (!active) continue;
+      // One row tile: the second warpgroup leaves its rows to the first, and its next weights wait
+      // until the first has read O_1.
+      const bool odd = !two && d.j1 - d.j0 > 1;  // there are rows in O_1
+      if (!two && t == 1) {
+        if (odd) {
+          sh.ml[row] = make_float2(m, l);
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) umma::mbar_arrive(smem_u32(&sh.hand[warp & 3]));
+          lent = true;
+        }
+        continue;
+      }
+      float f0 = 1.0f, f1 = 0.0f;
+      if (odd) {
+        if (!wait(smem_u32(&sh.hand[warp & 3]), hand_phase, abort_flag)) break;
+        hand_phase ^= 1;
+        umma::fence_after_sync();
+        const float2 other = sh.ml[row];  // (the wait above keeps the compiler from moving this)
+        const float mn = fmaxf(m, other.x);
+        f0 = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
+        f1 = other.x == -INFINITY ? 0.0f : ex2((other.x - mn) * c);
+        m = mn;
+        l = l * f0 + other.y * f1;
+      }
+      if (!active) {
+        __syncwarp();
+        if (odd && lane == 0) umma::mbar_arrive(smem_u32(&sh.back[warp & 3]));
+        if (narrow && d.j0 < d.j1 && lane == 0)
+          umma::mbar_arrive(smem_u32(&sh.out_done[(n_item - 1) & 1]));
+        continue;
+      }
       // Results leave through shared memory, 128 bytes of each row at a time (16-byte piece c of
       // row r at c ^ (r % 8)), so that a store covers whole lines: straight from a thread's own
       // row it would touch 32 of them.
@@ -783,39 +901,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                           : w.part + ((int64_t)d.slot * 2 * kTile + t * kTile) * kRowF<D>);
       const int64_t row_at = whole ? orow * D * 2
                              : (SHARED && d.j0 == 0 ? orow : (int64_t)row) * kRowF<D> * 4;
-      const uint32_t stage = kv_smem + C::STAGES * C::TILE + warp * kStage;
+      const uint32_t stage = (!narrow                ? base + 2 * C::TILE
+                              : is_small(d.n_tok) ? q_smem + C::HALVES * C::Q_SMALL
+                                                  : q_smem) +
+                             warp * kStage;
       const int passes = whole ? D / 64 : D / 32;
-#pragma unroll 1
-      for (int i = 0; i < passes; ++i) {
-        uint32_t o[2][16];
+      // 32 dims of the row from dim `at`, joined where there are two parts
+      auto result = [&](int at, uint32_t (&o)[2][16]) {
         if (d.j0 < d.j1) {
-          const uint32_t src = tm_o + (whole ? 64 : 32) * i;
-          umma::tmem_ld16_async(src, o[0]);
-          umma::tmem_ld16_async(src + 16, o[1]);
+          umma::tmem_ld16_async(tm_o + at, o[0]);
+          umma::tmem_ld16_async(tm_o + at + 16, o[1]);
           umma::tmem_wait_ld();
           umma::tmem_landed(o[0]);
           umma::tmem_landed(o[1]);
+          if (odd) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t x[16];
+              umma::tmem_ld16_async(tm_o + D + at + 16 * i, x);
+              umma::tmem_wait_ld();
+              umma::tmem_landed(x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[i][e] = __float_as_uint(
+                    fmaf(__uint_as_float(o[i][e]), f0, __uint_as_float(x[e]) * f1));
+            }
+          }
         }
         if (!(l > 0.0f)) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e >> 4][e & 15] = 0u;
         }
-        if (whole) {  // dims 64 i .. 64 i + 31, then the 32 behind them
-#pragma unroll
+      };
+#pragma unroll 1
+      for (int i = 0; i < passes; ++i) {
+        uint32_t o[2][16];
+        if (whole) {
+#pragma unroll 1
           for (int part = 0; part < 2; ++part) {
-            if (part) {
-              if (d.j0 < d.j1) {
-                umma::tmem_ld16_async(tm_o + 64 * i + 32, o[0]);
-                umma::tmem_ld16_async(tm_o + 64 * i + 48, o[1]);
-                umma::tmem_wait_ld();
-                umma::tmem_landed(o[0]);
-                umma::tmem_landed(o[1]);
-              }
-              if (!(l > 0.0f)) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e >> 4][e & 15] = 0u;
-              }
-            }
+            result(64 * i + 32 * part, o);
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
               uint32_t v[4];
@@ -828,11 +952,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
+          result(32 * i, o);
 #pragma unroll
           for (int q8 = 0; q8 < 8; ++q8)
             st_shared16(stage + lane * 128 + ((q8 ^ (lane & 7)) << 4),
                         o[q8 >> 2][4 * (q8 & 3)], o[q8 >> 2][4 * (q8 & 3) + 1],
                         o[q8 >> 2][4 * (q8 & 3) + 2], o[q8 >> 2][4 * (q8 & 3) + 3]);
+        }
+        if (odd && i == passes - 1) {  // O_1 has been read
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) umma::mbar_arrive(smem_u32(&sh.back[warp & 3]));
         }
         __syncwarp();
 #pragma unroll
@@ -849,6 +979,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float2*>(base_out + row_at + D * 4) = make_float2(mc, l);
         else if (p.lse)
           p.lse[orow] = l > 0.0f ? mc * kLn2 + logf(l) : -INFINITY;
+      }
+      if (narrow && d.j0 < d.j1) {  // (the copy of the next Q is another proxy's write)
+        umma::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(smem_u32(&sh.out_done[(n_item - 1) & 1]));
       }
     }
   }
@@ -928,8 +1063,8 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
     join_rows_kernel(const AttendParams p, const Work w, int ctas) {
   const int units = p.n_groups + p.B;
-  const int64_t total = w.line[units];
-  if (total < 0) return;
+  const int64_t wide = w.line[units], thin = w.line[units + 1];
+  if (wide < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hq = p.Hkv * p.G, tpt = kTile / p.G;
   const int64_t orow = (int64_t)blockIdx.x * kJoinRows + warp;
@@ -940,12 +1075,15 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (g < 0) return;
   const Unit own = load_unit<true>(p, p.n_groups + b);
   Join<D> a;
-  const int n_cta = share_count(total, ctas);
+  const int split = first_narrow(wide, thin, ctas);
 #pragma unroll 1
   for (int part = 0; part < 2 && !own.bad; ++part) {
     const int u = part ? p.n_groups + b : g;
     const Unit un = part ? own : load_unit<true>(p, g);
     if (un.n == 0) continue;
+    const int64_t total = un.narrow ? thin : wide;
+    const int cta0 = un.narrow ? split : 0;
+    const int n_cta = share_count(total, un.narrow ? ctas - split : split);
     const int t = (b - un.tok0) / (2 * tpt), i = (b - un.tok0) - t * 2 * tpt;
     const int r = i / tpt * kTile + i % tpt * p.G + (hq - h * p.G);  // the row within the item
     const int64_t cost = item_cost(un, tpt, t);
@@ -960,7 +1098,7 @@ __global__ void __launch_bounds__(kJoinThreads)
       const int j0 = cut_tile(x0 - pos, cost, wt, tiles), j1 = cut_tile(x1 - pos, cost, wt, tiles);
       if (j0 >= j1) continue;
       a.add(j0 == 0 ? w.first + ((part ? (int64_t)p.B * Hq : 0) + orow) * kRowF<D>
-                    : w.part + ((int64_t)c * 2 * kTile + r) * kRowF<D>,
+                    : w.part + ((int64_t)(cta0 + c) * 2 * kTile + r) * kRowF<D>,
             lane);
     }
   }
@@ -985,7 +1123,7 @@ size_t lay_out(const AttendParams& p, int ctas, void* ws, Work* w) {
   x.head = reinterpret_cast<Head*>(take(shared ? 0 : 2 * sizeof(Head) * ctas));
   x.part = reinterpret_cast<float*>(take((size_t)(shared ? 1 : 2) * ctas * 2 * kTile * row));
   x.first = reinterpret_cast<float*>(take(shared ? 2 * (size_t)p.B * p.Hkv * p.G * row : 0));
-  x.line = reinterpret_cast<int64_t*>(take(shared ? ((size_t)p.n_groups + p.B + 1) * 8 : 0));
+  x.line = reinterpret_cast<int64_t*>(take(shared ? ((size_t)p.n_groups + p.B + 2) * 8 : 0));
   if (w) *w = x;
   return at;
 }
@@ -1030,7 +1168,7 @@ cudaError_t launch(const AttendParams& p, const Work& w, int ctas, cudaStream_t 
   const int tpt = kTile / p.G;
   CUtensorMap q, q1, k, v;
   const int64_t qd[3] = {D, (int64_t)p.Hkv * p.G, p.T}, qs[2] = {D, p.sq_t};
-  const int qb[3] = {64, p.G, tpt}, qb1[3] = {64, p.G, 1};
+  const int qb[3] = {64, p.G, tpt}, qb1[3] = {64, p.G, kSmall / p.G};
   const int64_t kd[4] = {D, kPage, p.Hkv, p.kv.num_pages};
   const int64_t ks[3] = {p.kv.sk_t, p.kv.sk_h, p.kv.sk_p}, vs[3] = {p.kv.sv_t, p.kv.sv_h, p.kv.sv_p};
   const int kb[4] = {64, kPage, 1, 1};

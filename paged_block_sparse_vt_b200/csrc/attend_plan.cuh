@@ -7,6 +7,11 @@
 // takes the c-th of n equal lengths of the line.  A cut inside an item falls on the nearest key
 // tile and both neighbours compute it alike, so every tile has one owner, every CTA ends within
 // a tile's cost of the others, and a CTA has at most one item that began before it.
+//
+// There are two such lines, and the CTAs are dealt between them by their lengths.  Units of one
+// row tile (decode, drafted tokens, a prefix that few share) read their keys once for few rows:
+// they are bound by bytes, what they need is many of those in flight, and nearly all shared memory
+// of their CTAs goes to them.  All others need room for two tiles of queries and for results.
 #pragma once
 
 #include <stdint.h>
@@ -18,8 +23,9 @@ constexpr int kKeys = 128;  // keys of one step
 
 // Costs, in keys times a weight.  An item of one row tile takes less than one of two, but not
 // half: its keys are loaded all the same.
-constexpr int kCostTwo = 4, kCostOne = 3;
+constexpr int kCostTwo = 4, kCostOne = 3, kCostNarrow = 3;
 constexpr int kCostItem = 256;      // loading q, filling the pipeline, writing out
+constexpr int kCostItemNarrow = 128;
 constexpr int64_t kMinShare = 4 * kKeys * kCostTwo;  // no CTA takes less than four key tiles
 
 struct Unit {
@@ -29,6 +35,7 @@ struct Unit {
   int kv_len;      // keys there are, from page `page0` of table row `row`
   int page0, row;
   bool bad;        // a bad length: no keys, empty rows
+  bool narrow;
 };
 
 #define VT_HD __host__ __device__ __forceinline__
@@ -44,11 +51,12 @@ VT_HD int item_keys(const Unit& u, int tpt, int t) {
 }
 
 VT_HD int item_weight(const Unit& u, int tpt, int t) {
-  return u.n - t * 2 * tpt > tpt ? kCostTwo : kCostOne;
+  return u.narrow ? kCostNarrow : u.n - t * 2 * tpt > tpt ? kCostTwo : kCostOne;
 }
 
 VT_HD int64_t item_cost(const Unit& u, int tpt, int t) {
-  return (int64_t)item_weight(u, tpt, t) * (kCostItem + item_keys(u, tpt, t));
+  return (int64_t)item_weight(u, tpt, t) *
+         ((u.narrow ? kCostItemNarrow : kCostItem) + item_keys(u, tpt, t));
 }
 
 // Cost of a head's items before t <= unit_items; all but the last item have two full tiles.
@@ -68,6 +76,14 @@ VT_HD int cut_tile(int64_t x, int64_t cost, int weight, int n_tiles) {
   if (x >= cost) return n_tiles;
   const int64_t t = (x / weight + kKeys / 2) / kKeys;
   return t < n_tiles ? (int)t : n_tiles;
+}
+
+// The CTAs from which on the narrow line is worked on.
+VT_HD int first_narrow(int64_t wide, int64_t narrow, int ctas) {
+  if (narrow == 0) return ctas;
+  if (wide == 0) return 0;
+  const int n = (int)((double)narrow / (double)(wide + narrow) * ctas + 0.5);
+  return ctas - (n < 1 ? 1 : n > ctas - 1 ? ctas - 1 : n);
 }
 
 // CTAs that share a line of length `total`, and where the c-th share begins.
