@@ -31,6 +31,7 @@
 #include "attend_params.cuh"
 #include "attend_plan.cuh"
 #include "common.cuh"
+#include "gqa_attend.cuh"
 #include "umma.cuh"
 
 namespace vt {
@@ -42,13 +43,12 @@ constexpr int kThreads = 384;   // two softmax warpgroups, and one with the load
 // third warpgroup gives up goes to the other two (2 * 200 + 104 = 3 * 168, the launch's share).
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kDescs = 6;       // items described ahead
+constexpr int kDescs = 4;       // items described ahead
 constexpr int kBadRing = 16;    // key tiles whose page checks are kept (> tiles in flight)
 constexpr int kPlan = 1024;     // entries of the cost table in shared memory
 constexpr float kLazy = 8.0f;
 constexpr int kPagesTile = kKeys / kPage;
 constexpr int kSoftWarps = 8;
-constexpr int kSmall = 32;      // rows of a small item
 constexpr int kStage = 32 * 128;  // a softmax warp's staging: 128 bytes of each of its rows
 
 template <int D>
@@ -56,17 +56,11 @@ struct Cfg {
   static constexpr int HALVES = D / 64;              // 64-dim boxes of a row
   static constexpr int BOX = kKeys * 128;            // bytes of one half of a tile
   static constexpr int TILE = HALVES * BOX;          // bytes of a Q, K or V tile
-  // wide: two Q tiles, 128 KB of K and V, staging of all softmax warps
   static constexpr int STAGES = D == 128 ? 4 : 8;
-  static constexpr int WIDE = 2 * TILE + kSoftWarps * kStage + STAGES * TILE;
-  // narrow: one Q tile, 192 KB of K and V.  Items of up to kSmall rows fill only the first of the
-  // four parts of that tile; the second stages their results.  (The product reads 128 rows of Q
-  // all the same; the others are what stands there, and nobody looks at their results.)  Larger
-  // ones stage theirs over their own Q, so the next Q waits for them.
-  static constexpr int Q_SMALL = kSmall * 128;  // bytes of one half
-  static constexpr int STAGES_NARROW = D == 128 ? 6 : 12;
-  static constexpr int NARROW = TILE + STAGES_NARROW * TILE;
-  static constexpr int SMEM = 1024 + (WIDE > NARROW ? WIDE : NARROW);
+  static constexpr int TILES_SMEM = 2 * TILE + STAGES * TILE + kSoftWarps * kStage;
+  // a CTA of the second line: each warp's two pages in flight
+  static constexpr int OWN_SMEM = kWarps * 2 * PageTile<D>::SLOT;
+  static constexpr int SMEM = 1024 + (TILES_SMEM > OWN_SMEM ? TILES_SMEM : OWN_SMEM);
 };
 
 // What the loading warp tells the others about a piece of an item.
@@ -79,7 +73,6 @@ struct Desc {
   int kv_len;          // valid keys
   int slot;            // where a partial result goes: -1 none (write out), else see below
   int whole;           // 1: all key tiles
-  int prefix;          // the item is a shared prefix
 };
 
 // A header of a partial slot.
@@ -93,6 +86,7 @@ struct Work {          // the workspace
                        //   2c + 1 begins one; shared prefixes: [ctas][256][D + 4], slot c continues
   float* first;        // shared prefixes: [2][B Hq][D + 4], the rows of items' first pieces:
                        //   prefixes, then own pages
+  float* own;          // shared prefixes: [ctas kWarps][8][D + 4]: rows that a warp's share continues
   int64_t* line;       // shared prefixes: [units + 2] where each unit begins in its line, and the
                        //   lengths of the two lines
 };
@@ -105,18 +99,12 @@ struct Shared {
   Desc desc[kDescs];
   int bad[kBadRing];
   uint64_t q_full, q_empty, s_full[2], p_ready[2][2], o_full[2], desc_full[kDescs],
-      desc_empty[kDescs], kv_full[12], kv_empty[12], hand[4], back[4], out_done[2], drain;
-  float2 ml[kTile];  // m and l of the second warpgroup's rows, where it shares the first's
+      desc_empty[kDescs], kv_full[8], kv_empty[8], drain;
   uint32_t tmem;
   int abort;
 };
 
 // ---- the units ------------------------------------------------------------------------------
-
-template <bool SHARED>
-__device__ __forceinline__ int unit_count(const AttendParams& p) {
-  return SHARED ? p.n_groups + p.B : p.B;
-}
 
 // The group of request b, or -1: groups are few and their starts stay in L1.
 __device__ __forceinline__ int group_of(const AttendParams& p, int b) {
@@ -137,7 +125,7 @@ __device__ __forceinline__ int group_prefix(const AttendParams& p, int g) {
 }
 
 template <bool SHARED>
-__device__ Unit load_unit_raw(const AttendParams& p, int u) {
+__device__ Unit load_unit(const AttendParams& p, int u) {
   Unit x{};
   if (!SHARED) {
     const int len = p.seq_lens[u];
@@ -165,13 +153,6 @@ __device__ Unit load_unit_raw(const AttendParams& p, int u) {
     x.page0 = max(pages, 0);
     x.kv_len = x.vis0 = x.bad ? 0 : len - x.page0 * kPage;
   }
-  return x;
-}
-
-template <bool SHARED>
-__device__ __forceinline__ Unit load_unit(const AttendParams& p, int u) {
-  Unit x = load_unit_raw<SHARED>(p, u);
-  x.narrow = x.n <= kTile / p.G;
   return x;
 }
 
@@ -273,6 +254,147 @@ struct RowMask {
   }
 };
 
+// ---- a decode row's own pages ---------------------------------------------------------------
+
+// Where a warp is in the second line: the item (request b, KV head h), its place and its pages.
+struct OwnCursor {
+  int b, h, pages;
+  int64_t pos, cost;
+  Unit un;
+
+  __device__ __forceinline__ void take(const AttendParams& p, int b_) {
+    b = b_;
+    un = load_unit<true>(p, p.n_groups + b);
+    pages = own_pages(un);
+    cost = own_cost(un);
+  }
+  // The item that position x0 (below the line's end) is in.
+  __device__ void seek(const AttendParams& p, const int64_t* table, int entries, int per,
+                       int64_t x0) {
+    int lo = 0, hi = entries - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (table[mid] <= x0) lo = mid; else hi = mid - 1;
+    }
+    pos = table[lo];
+    take(p, max(0, lo * per - p.n_groups));
+    while (pos + p.Hkv * cost <= x0) {
+      pos += p.Hkv * cost;
+      take(p, b + 1);
+    }
+    h = (int)((x0 - pos) / cost);
+    pos += h * cost;
+  }
+  __device__ __forceinline__ void next(const AttendParams& p) {
+    pos += cost;
+    if (++h < p.Hkv) return;
+    h = 0;
+    do {
+      if (b + 1 == p.B) {
+        pos = INT64_MAX;  // behind every share
+        return;
+      }
+      take(p, b + 1);
+    } while (cost == 0);
+  }
+};
+
+// One warp's share [x0, x1) of the second line: the pages one after the other, two of them in
+// flight in its two slots of shared memory, across items too.
+template <int D>
+__device__ __forceinline__ void own_share(const AttendParams& p, const Work& w, OwnCursor cur,
+                                          int64_t x0, int64_t x1, uint32_t smem, int ws, int lane) {
+  using T = PageTile<D>;
+  const int Hq = p.Hkv * p.G;
+  const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(p.kv.k_pool);
+  const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(p.kv.v_pool);
+  struct Slot {
+    int vr;  // valid tokens, -1: nothing staged
+    bool first, last;
+    const __nv_bfloat16* q;
+    float* dst;
+  };
+  int i = 0, i0 = 0, i1 = 0, ids = -1, ids_next = -1;
+  const int32_t* table = nullptr;
+  float* dst = nullptr;
+  auto id_at = [&](int k) { return k + lane < i1 ? table[k + lane] : -1; };
+  auto find = [&]() {  // the next item with pages in this share
+    while (cur.pos < x1) {
+      i = i0 = own_cut(x0 - cur.pos, cur.pages);
+      i1 = own_cut(x1 - cur.pos, cur.pages);
+      if (i < i1) {
+        table = p.page_table + (int64_t)cur.un.row * p.pt_stride + cur.un.page0;
+        dst = i == 0 ? w.first + ((int64_t)p.B * Hq + (int64_t)cur.b * Hq + cur.h * p.G) * kRowF<D>
+                     : w.own + (int64_t)ws * 8 * kRowF<D>;
+        ids_next = id_at(i);
+        return true;
+      }
+      cur.next(p);
+    }
+    return false;
+  };
+  bool more = find();
+  auto stage = [&](Slot& s, uint32_t slot) {
+    s.vr = -1;
+    if (more) {
+      if (((i - i0) & 31) == 0) {
+        ids = ids_next;
+        ids_next = id_at(i + 32);
+      }
+      const int id = __shfl_sync(kFull, ids, (i - i0) & 31);
+      s.vr = min(kPage, cur.un.kv_len - kPage * i);
+      s.first = i == i0;
+      s.last = i + 1 == i1;
+      s.q = p.q + cur.b * p.sq_t + (int64_t)cur.h * p.G * D;
+      s.dst = dst;
+      int page = id;
+      if (id < 0 || id >= p.kv.num_pages) {
+        if (lane == 0) flag(p.status, VT_DEV_BAD_PAGE);
+        s.vr = page = 0;
+      }
+      stage_page<D>(slot, kp + page * p.kv.sk_p + cur.h * p.kv.sk_h,
+                    vp + page * p.kv.sv_p + cur.h * p.kv.sv_h, p.kv.sk_t, p.kv.sv_t, s.vr, p.q,
+                    lane);
+      if (++i == i1) {
+        cur.next(p);
+        more = find();
+      }
+    }
+    cp_async_commit();
+  };
+  WarpAttention<D, 8> wa;
+  auto attend = [&](const Slot& s, uint32_t slot) {
+    cp_async_wait<1>();
+    __syncwarp();
+    if (s.first) wa.init(s.q, lane, p.G);
+    wa.template page<false>(slot, s.vr, p.qscale);
+    if (s.last) {
+      float l = wa.lrun;
+      l += __shfl_xor_sync(kFull, l, 1);
+      l += __shfl_xor_sync(kFull, l, 2);
+      if (wa.g < p.G) {
+        float* r = s.dst + wa.g * kRowF<D>;
+#pragma unroll
+        for (int t = 0; t < T::NT; ++t)
+          *reinterpret_cast<float2*>(r + t * 8 + wa.qd) = make_float2(wa.o[t][0], wa.o[t][1]);
+        if ((lane & 3) == 0) *reinterpret_cast<float2*>(r + D) = make_float2(wa.mrun, l);
+      }
+    }
+    __syncwarp();
+  };
+  Slot s0, s1;
+  stage(s0, smem);
+  stage(s1, smem + T::SLOT);
+  while (s0.vr >= 0) {
+    attend(s0, smem);
+    stage(s0, smem);
+    if (s1.vr < 0) break;
+    attend(s1, smem + T::SLOT);
+    stage(s1, smem + T::SLOT);
+  }
+  cp_async_wait_all();
+}
+
 // ---- the kernel -----------------------------------------------------------------------------
 
 template <int N>
@@ -287,13 +409,13 @@ __device__ __forceinline__ void regs_less() {
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const AttendParams p, const Work w, const __grid_constant__ CUtensorMap q_map,
-                  const __grid_constant__ CUtensorMap q1_map,
                   const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map) {
   using C = Cfg<D>;
   extern __shared__ unsigned char raw[];
   __shared__ Shared sh;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t q_smem = base, kv_smem = base + 2 * C::TILE;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpt = kTile / p.G;
   const int cta = blockIdx.x;
@@ -303,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* table1 = table0 + kPlan + 1;
 
   // The starts, then the cost of every unit, summed up over entries of `per` units each.
-  const int units = unit_count<SHARED>(p);
+  const int units = SHARED ? p.n_groups + p.B : p.B, tile_units = SHARED ? p.n_groups : p.B;
   const int n_start = SHARED ? p.n_groups : p.B;
   bool fine = true;
   for (int i = threadIdx.x; i < n_start; i += kThreads)
@@ -314,8 +436,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh.abort = 0;
     umma::mbar_init(smem_u32(&sh.q_full), 1);
     umma::mbar_init(smem_u32(&sh.q_empty), 1);
-    umma::mbar_init(smem_u32(&sh.out_done[0]), 4);
-    umma::mbar_init(smem_u32(&sh.out_done[1]), 4);
     umma::mbar_init(smem_u32(&sh.drain), 1);
     for (int t = 0; t < 2; ++t) {
       umma::mbar_init(smem_u32(&sh.s_full[t]), 1);
@@ -323,15 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma::mbar_init(smem_u32(&sh.p_ready[t][1]), 4);
       umma::mbar_init(smem_u32(&sh.o_full[t]), 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      umma::mbar_init(smem_u32(&sh.hand[i]), 1);
-      umma::mbar_init(smem_u32(&sh.back[i]), 1);
-    }
     for (int i = 0; i < kDescs; ++i) {
       umma::mbar_init(smem_u32(&sh.desc_full[i]), 1);
       umma::mbar_init(smem_u32(&sh.desc_empty[i]), 9);
     }
-    for (int i = 0; i < 12; ++i) {
+    for (int i = 0; i < C::STAGES; ++i) {
       umma::mbar_init(smem_u32(&sh.kv_full[i]), 1);
       umma::mbar_init(smem_u32(&sh.kv_empty[i]), 1);
     }
@@ -349,13 +465,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = e * per; u < min(units, (e + 1) * per); ++u) {
         const Unit x = load_unit<SHARED>(p, u);
         if (x.bad && cta == 0) flag(p.status, VT_DEV_BAD_LEN);
-        c[x.narrow] += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
+        if (SHARED && u >= p.n_groups) c[1] += p.Hkv * own_cost(x);
+        else c[0] += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
       }
       table0[e + 1] = c[0];
-      table1[e + 1] = c[1];
+      if (SHARED) table1[e + 1] = c[1];
     }
   __syncthreads();
-  if (fine && warp < 2) {
+  if (fine && warp < (SHARED ? 2 : 1)) {
     int64_t* line = warp ? table1 : table0;
     const int run = (entries + 31) / 32;
     int64_t sum = 0;
@@ -376,14 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   if (!fine && cta == 0 && threadIdx.x == 0) flag(p.status, VT_DEV_BAD_START);
-  const int64_t wide = fine ? table0[entries] : 0, thin = fine ? table1[entries] : 0;
-  // this CTA's line, its number there and how many share it
-  const int split = first_narrow(wide, thin, gridDim.x);
-  const bool narrow = cta >= split;
-  const int64_t* line = narrow ? table1 : table0;
-  const int64_t total = narrow ? thin : wide;
-  const int rank = narrow ? cta - split : cta;
-  const int n_cta = share_count(total, narrow ? gridDim.x - split : split);
+  const int64_t total = fine ? table0[entries] : 0, pages = SHARED && fine ? table1[entries] : 0;
+  const int split = SHARED ? first_own(total, pages, gridDim.x) : gridDim.x;
+  const int n_cta = share_count(total, max(split, 1), kMinShare);
 
   if (SHARED && cta == 0) {  // where the units begin, for the joining kernel; -1: nothing was done
     if (fine) {
@@ -391,25 +503,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t c[2] = {table0[e], table1[e]};
         for (int u = e * per; u < min(units, (e + 1) * per); ++u) {
           const Unit x = load_unit<SHARED>(p, u);
-          w.line[u] = c[x.narrow];
-          c[x.narrow] += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
+          w.line[u] = c[u >= p.n_groups];
+          if (u >= p.n_groups) c[1] += p.Hkv * own_cost(x);
+          else c[0] += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
         }
       }
     }
     if (threadIdx.x == 0) {
-      w.line[units] = fine ? wide : -1;
-      w.line[units + 1] = thin;
+      w.line[units] = fine ? total : -1;
+      w.line[units + 1] = pages;
     }
     __syncthreads();  // (before q overwrites the tables)
   }
 
-  // shared memory of the two kinds
-  const uint32_t q_smem = base;
-  const uint32_t kv_smem = base + (narrow ? C::TILE : 2 * C::TILE + kSoftWarps * kStage);
-  auto is_small = [&](int n_tok) { return narrow && n_tok * p.G <= kSmall; };
-  const int stages = narrow ? C::STAGES_NARROW : C::STAGES;
+  if (SHARED && cta >= split) {
+    // ---- own pages: a warp, a share ------------------------------------------------------------
+    const int n_warp = share_count(pages, (gridDim.x - split) * kWarps, kMinPages);
+    const int ws = (cta - split) * kWarps + warp;
+    const int64_t x0 = ws < n_warp ? share_begin(pages, n_warp, ws) : 0;
+    const int64_t x1 = ws < n_warp ? share_begin(pages, n_warp, ws + 1) : 0;
+    OwnCursor cur;
+    if (x0 < x1) cur.seek(p, table1, entries, per, x0);
+    __syncthreads();  // (before the pages overwrite the tables)
+    if (x0 < x1) own_share<D>(p, w, cur, x0, x1, base + warp * 2 * PageTile<D>::SLOT, ws, lane);
+    __syncthreads();
+    if (warp == kMmaWarp) umma::tmem_dealloc(tm, 512);
+    return;
+  }
 
-  const bool work = total > 0 && rank < n_cta;
+  const int64_t* line = table0;
+  const bool work = total > 0 && cta < n_cta;
   if (warp >= kLoadWarp) {
   regs_less<kRegsOther>();
   if (warp == kLoadWarp) {
@@ -419,13 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.head[2 * cta + 1].valid = 0;
     }
     int n_desc = 0, n_item = 0, n_tile = 0;
-    int n_out = 0;        // items whose results are known to be out
-    bool small_before = true;
-    int st = 0;           // the ring's next stage and its phase
-    uint32_t ph = 0, filled = 0;
+    uint32_t filled = 0;  // stage uses, for the drain behind an abort
     bool go = true;
     if (work) {
-      const int64_t x0 = share_begin(total, n_cta, rank), x1 = share_begin(total, n_cta, rank + 1);
+      const int64_t x0 = share_begin(total, n_cta, cta), x1 = share_begin(total, n_cta, cta + 1);
       int lo = 0, hi = entries - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -434,12 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int u = lo * per;
       int64_t pos = line[lo];
       Unit un = load_unit<SHARED>(p, u);
-      int items = un.narrow == narrow ? unit_items(un, tpt) : 0;
+      int items = unit_items(un, tpt);
       int64_t head_cost = cost_before(un, tpt, items);
       while (pos + p.Hkv * head_cost <= x0) {  // x0 < total, so this ends at a unit with items
         pos += p.Hkv * head_cost;
         un = load_unit<SHARED>(p, ++u);
-        items = un.narrow == narrow ? unit_items(un, tpt) : 0;
+        items = unit_items(un, tpt);
         head_cost = cost_before(un, tpt, items);
       }
       int h = (int)((x0 - pos) / head_cost);
@@ -467,7 +587,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!go) break;
           const int first = t * 2 * tpt, n_tok = min(un.n - first, 2 * tpt);
           const bool whole = j0 == 0 && j1 == tiles;
-          const bool prefix = SHARED && u < p.n_groups;
           if (lane == 0) {
             Desc d;
             d.tok0 = un.tok0 + first;
@@ -479,7 +598,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             d.step = un.step;
             d.kv_len = un.kv_len;
             d.whole = whole;
-            d.prefix = prefix;
             d.slot = SHARED ? cta : whole ? -1 : 2 * cta + (j0 == 0);
             sh.desc[di] = d;
             if (!SHARED && !whole) {
@@ -521,8 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
+              const int use = 2 * n_tile + kv, st = use % C::STAGES;
               const uint32_t full = smem_u32(&sh.kv_full[st]);
-              go = go && wait(smem_u32(&sh.kv_empty[st]), ph ^ 1, abort_flag);
+              go = go && wait(smem_u32(&sh.kv_empty[st]), ((use / C::STAGES) & 1) ^ 1, abort_flag);
               if (!go) break;
               if (lane == 0) umma::mbar_expect_tx(full, C::TILE);
               __syncwarp();
@@ -533,33 +652,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   kv ? &v_map : &k_map, half * 64, c_tok, h, id, full);
               }
               ++filled;
-              if (++st == stages) {
-                st = 0;
-                ph ^= 1;
-              }
               if (kv == 0 && j == j0) {
                 // q goes behind the first K tile: its buffer is free only when the last item's
                 // scores are done
                 go = wait(smem_u32(&sh.q_empty), (n_item & 1) ^ 1, abort_flag);
                 if (!go) break;
                 const int tiles_q = n_tok > tpt ? 2 : 1;
-                const bool small = is_small(n_tok);
-                // results out: of the last item where the two meet in shared memory, else of the
-                // one before, so that no phase of the two barriers is passed unseen
-                const int outs = !narrow ? 0 : small && small_before ? n_item - 1 : n_item;
-                for (; go && n_out < outs; ++n_out)
-                  go = wait(smem_u32(&sh.out_done[n_out & 1]), n_out >> 1 & 1, abort_flag);
-                if (!go) break;
-                small_before = small;
                 if (lane == 0) {
                   const uint32_t bar = smem_u32(&sh.q_full);
-                  const int box = p.G * (small ? kSmall / p.G : tpt) * 128;
-                  umma::mbar_expect_tx(bar, box * C::HALVES * tiles_q);
+                  umma::mbar_expect_tx(bar, p.G * tpt * 128 * C::HALVES * tiles_q);
                   for (int tt = 0; tt < tiles_q; ++tt)
                     for (int half = 0; half < C::HALVES; ++half)
-                      umma::tma_load_3d(q_smem + tt * C::TILE + half * (small ? C::Q_SMALL : C::BOX),
-                                        small ? &q1_map : &q_map, half * 64, h * p.G,
-                                        un.tok0 + first + tt * tpt, bar);
+                      umma::tma_load_3d(q_smem + tt * C::TILE + half * C::BOX, &q_map, half * 64,
+                                        h * p.G, un.tok0 + first + tt * tpt, bar);
                 }
                 ++n_item;
               }
@@ -573,11 +678,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++h == p.Hkv) {
             h = 0;
             do {
-              if (++u == units) break;
+              if (++u == tile_units) break;
               un = load_unit<SHARED>(p, u);
-              items = un.narrow == narrow ? unit_items(un, tpt) : 0;
+              items = unit_items(un, tpt);
             } while (items == 0);
-            if (u == units) break;
+            if (u == tile_units) break;
           }
         }
       }
@@ -591,13 +696,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!go) {  // copies in flight must land before the shared memory goes away
-      for (uint32_t i = 0; i < min(filled, (uint32_t)stages); ++i) {
-        if (st-- == 0) {
-          st = stages - 1;
-          ph ^= 1;
-        }
+      for (uint32_t i = 0; i < min(filled, (uint32_t)C::STAGES); ++i) {
+        const uint32_t use = filled - 1 - i;
         const unsigned long long t0 = global_ns();
-        while (!umma::mbar_try_wait(smem_u32(&sh.kv_full[st]), ph) && global_ns() - t0 < kWaitNs) {
+        while (!umma::mbar_try_wait(smem_u32(&sh.kv_full[use % C::STAGES]),
+                                    (use / C::STAGES) & 1) &&
+               global_ns() - t0 < kWaitNs) {
         }
       }
       const unsigned long long t0 = global_ns();
@@ -609,19 +713,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- products ----------------------------------------------------------------------------
     constexpr uint32_t kIdS = umma::idesc_bf16(kTile, kKeys, false, false);
     constexpr uint32_t kIdO = umma::idesc_bf16(kTile, D, false, true);
-    int n_desc = 0, n_item = 0;
-    int k_st = 0, v_st = 1;  // the ring's next K and V stage, and their phases
-    uint32_t k_ph = 0, v_ph = 0, p_phase[2] = {0, 0};
+    int n_desc = 0, n_item = 0, n_tile = 0;
+    uint32_t p_phase[2] = {0, 0};
     bool go = true;
-    auto scores = [&](int t, int q_tile, uint32_t q_half, int st) {
+    auto scores = [&](int t, int st) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t at = (k % 4) * 32;
-        umma::mma_bf16(
-            tm + t * kKeys,
-            umma::sdesc_sw128(q_smem + q_tile * C::TILE + (k / 4) * q_half + at, 0, 1024),
-            umma::sdesc_sw128(kv_smem + st * C::TILE + (k / 4) * C::BOX + at, 0, 1024), kIdS,
-            k > 0);
+        const uint32_t off = (k / 4) * C::BOX + (k % 4) * 32;
+        umma::mma_bf16(tm + t * kKeys,
+                       umma::sdesc_sw128(q_smem + t * C::TILE + off, 0, 1024),
+                       umma::sdesc_sw128(kv_smem + st * C::TILE + off, 0, 1024), kIdS, k > 0);
       }
       umma::commit(smem_u32(&sh.s_full[t]));
     };
@@ -642,52 +743,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n_desc;
       if (n_tok == 0) break;
       if (j0 == j1) continue;
-      // Step k: the values of key tile k - lag, then the scores of key tile k.  Two row tiles take
-      // every key tile one after the other.  One row tile alone would leave the tensor cores
-      // idle while its softmax runs, so it takes key tiles in turn as two: even ones in S_0 and
-      // O_0, odd ones in S_1 and O_1, each with its own maxima and sums, joined at the end.
-      const bool two = n_tok > tpt;
-      const int n = j1 - j0, lag = two ? 1 : 2;
-      const uint32_t q_half = is_small(n_tok) ? C::Q_SMALL : C::BOX;
-      go = wait(smem_u32(&sh.q_full), n_item & 1, abort_flag);
-      for (int k = 0; go && k < n + lag; ++k) {
-        const bool has_k = k < n, has_v = k >= lag && k - lag < n;
-        if (has_k)
-          go = wait(smem_u32(&sh.kv_full[k_st]), k_ph, abort_flag);
-        if (go && has_v) go = wait(smem_u32(&sh.kv_full[v_st]), v_ph, abort_flag);
-        const int t0 = two ? 0 : k & 1, t1 = two ? 1 : t0;
-        for (int t = t0; go && t <= t1; ++t) {
-          if (has_v) {
+      const int nt = n_tok > tpt ? 2 : 1;
+      for (int j = j0; go && j <= j1; ++j) {
+        // step j: the values of tile j - 1, then the scores of tile j, row tile by row tile
+        const int kst = 2 * n_tile % C::STAGES, vst = (2 * n_tile - 1) % C::STAGES;
+        if (j == j0) go = wait(smem_u32(&sh.q_full), n_item & 1, abort_flag);
+        if (go && j < j1)
+          go = wait(smem_u32(&sh.kv_full[kst]), (2 * n_tile / C::STAGES) & 1, abort_flag);
+        if (go && j > j0)
+          go = wait(smem_u32(&sh.kv_full[vst]), ((2 * n_tile - 1) / C::STAGES) & 1, abort_flag);
+        for (int t = 0; go && t < nt; ++t) {
+          if (j > j0) {
             go = wait(smem_u32(&sh.p_ready[t][0]), p_phase[t], abort_flag);
             if (!go) break;
             umma::fence_after_sync();
-            values(t, v_st, 0, k >= 2 * lag);
+            values(t, vst, 0, j > j0 + 1);
             go = wait(smem_u32(&sh.p_ready[t][1]), p_phase[t], abort_flag);
             if (!go) break;
             umma::fence_after_sync();
-            values(t, v_st, 1, true);
+            values(t, vst, 1, true);
             p_phase[t] ^= 1;
-            if (!has_k) umma::commit(smem_u32(&sh.o_full[t]));
+            if (j == j1) umma::commit(smem_u32(&sh.o_full[t]));
           } else {
             umma::fence_after_sync();
           }
-          if (has_k) scores(t, two ? t : 0, q_half, k_st);
+          if (j < j1) scores(t, kst);
         }
         if (!go) break;
-        if (has_v) {
-          umma::commit(smem_u32(&sh.kv_empty[v_st]));
-          if ((v_st += 2) >= stages) {
-            v_st = 1;
-            v_ph ^= 1;
-          }
-        }
-        if (has_k) {
-          umma::commit(smem_u32(&sh.kv_empty[k_st]));
-          if (k == n - 1) umma::commit(smem_u32(&sh.q_empty));
-          if ((k_st += 2) >= stages) {
-            k_st = 0;
-            k_ph ^= 1;
-          }
+        if (j > j0) umma::commit(smem_u32(&sh.kv_empty[vst]));
+        if (j < j1) {
+          umma::commit(smem_u32(&sh.kv_empty[kst]));
+          if (j == j1 - 1) umma::commit(smem_u32(&sh.q_empty));
+          ++n_tile;
         }
       }
       if (!go) break;
@@ -709,9 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.qscale, lazy = kLazy / c;
     const int Hq = p.Hkv * p.G;
     const int tok_row = row / p.G, head_row = row - tok_row * p.G;
-    uint32_t s_phase = 0, o_phase = 0, hand_phase = 0;
-    bool lent = false;  // O_1 is the first warpgroup's to read
-    int n_tile = 0, n_item = 0;
+    uint32_t s_phase = 0, o_phase = 0;
+    int n_tile = 0;
     for (int n_desc = 0;; ++n_desc) {
       const int di = n_desc % kDescs;
       if (!wait(smem_u32(&sh.desc_full[di]), (n_desc / kDescs) & 1, abort_flag)) break;
@@ -719,25 +805,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) umma::mbar_arrive(smem_u32(&sh.desc_empty[di]));
       if (d.n_tok == 0) break;
-      const bool two = d.n_tok > tpt;
-      const int rt = two ? t : 0;  // row tile
-      const int n_tok = min(tpt, d.n_tok - rt * tpt);
-      const bool active = (warp & 3) * 32 < n_tok * p.G, mine = row < n_tok * p.G;
-      const int tok = rt * tpt + min(tok_row, n_tok - 1);
+      const int n_tok = min(tpt, d.n_tok - t * tpt);
+      if (n_tok <= 0) {
+        n_tile += d.j1 - d.j0;
+        continue;
+      }
+      const bool active = (warp & 3) * 32 < n_tok * p.G;
+      const int tok = t * tpt + min(tok_row, n_tok - 1);
       const int vis = d.vis0 + tok * d.step;
-      const int vis_warp = d.vis0 + (rt * tpt + min((warp & 3) * 32 / p.G, n_tok - 1)) * d.step;
+      const int vis_warp = d.vis0 + (t * tpt + min((warp & 3) * 32 / p.G, n_tok - 1)) * d.step;
       const int n_pages = (d.kv_len + kPage - 1) / kPage;
       const int gap = n_pages * kPage - d.kv_len;   // zero rows ahead of the last page's tokens
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
-      const int begin = two ? d.j0 : d.j0 + t, stride = two ? 1 : 2;
-      for (int j = begin; j < d.j1; j += stride) {
+      for (int j = d.j0; j < d.j1; ++j, ++n_tile) {
         ok = wait(smem_u32(&sh.s_full[t]), s_phase, abort_flag);
         if (!ok) break;
         s_phase ^= 1;
         if (active) {
           umma::fence_after_sync();
-          const uint32_t bad = (uint32_t)*(volatile int*)&sh.bad[(n_tile + j - d.j0) % kBadRing];
+          const uint32_t bad = (uint32_t)*(volatile int*)&sh.bad[n_tile % kBadRing];
           const int slot0 = j * kKeys;
           const bool masked = slot0 + kKeys > vis_warp || bad;
           if (masked) {  // what a row may not see becomes -inf in place
@@ -783,12 +870,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t s[2][32];
           umma::tmem_ld32_async(tm_s, s[0]);
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (__any_sync(kFull, mine && (top > m + lazy || (m == -INFINITY && top > m)))) {
+          if (__any_sync(kFull, top > m + lazy || (m == -INFINITY && top > m))) {
             const float mn = fmaxf(m, top);
             const float f = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
             m = mn;
             l *= f;
-            if (j > begin) {
+            if (j > d.j0) {
 #pragma unroll 1
               for (int i = 0; i < D / 16; ++i) {
                 uint32_t o[16];
@@ -819,11 +906,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             umma::tmem_st16_async(tm_s + 16 * i, pk);  // (over scores that were read)
             if (i & 1) {  // half of the keys: the product with their values can start
-              if (lent) {
-                wait(smem_u32(&sh.back[warp & 3]), hand_phase, abort_flag);
-                hand_phase ^= 1;
-                lent = false;
-              }
               umma::tmem_wait_st();
               umma::fence_before_sync();
               __syncwarp();
@@ -831,58 +913,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           l += total2(sum[0], sum[1]);
-        } else {
-          if (lent) {
-            wait(smem_u32(&sh.back[warp & 3]), hand_phase, abort_flag);
-            hand_phase ^= 1;
-            lent = false;
-          }
-          if (lane == 0) {
-            umma::mbar_arrive(smem_u32(&sh.p_ready[t][0]));
-            umma::mbar_arrive(smem_u32(&sh.p_ready[t][1]));
-          }
+        } else if (lane == 0) {
+          umma::mbar_arrive(smem_u32(&sh.p_ready[t][0]));
+          umma::mbar_arrive(smem_u32(&sh.p_ready[t][1]));
         }
       }
       if (!ok) break;
-      n_tile += d.j1 - d.j0;
-      n_item += d.j0 < d.j1;
-      if (begin < d.j1) {
+      if (d.j0 < d.j1) {
         if (!wait(smem_u32(&sh.o_full[t]), o_phase, abort_flag)) break;
         o_phase ^= 1;
         umma::fence_after_sync();
       }
-      // One row tile: the second warpgroup leaves its rows to the first, and its next weights wait
-      // until the first has read O_1.
-      const bool odd = !two && d.j1 - d.j0 > 1;  // there are rows in O_1
-      if (!two && t == 1) {
-        if (odd) {
-          sh.ml[row] = make_float2(m, l);
-          umma::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) umma::mbar_arrive(smem_u32(&sh.hand[warp & 3]));
-          lent = true;
-        }
-        continue;
-      }
-      float f0 = 1.0f, f1 = 0.0f;
-      if (odd) {
-        if (!wait(smem_u32(&sh.hand[warp & 3]), hand_phase, abort_flag)) break;
-        hand_phase ^= 1;
-        umma::fence_after_sync();
-        const float2 other = sh.ml[row];  // (the wait above keeps the compiler from moving this)
-        const float mn = fmaxf(m, other.x);
-        f0 = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
-        f1 = other.x == -INFINITY ? 0.0f : ex2((other.x - mn) * c);
-        m = mn;
-        l = l * f0 + other.y * f1;
-      }
-      if (!active) {
-        __syncwarp();
-        if (odd && lane == 0) umma::mbar_arrive(smem_u32(&sh.back[warp & 3]));
-        if (narrow && d.j0 < d.j1 && lane == 0)
-          umma::mbar_arrive(smem_u32(&sh.out_done[(n_item - 1) & 1]));
-        continue;
-      }
+      if (!active) continue;
       // Results leave through shared memory, 128 bytes of each row at a time (16-byte piece c of
       // row r at c ^ (r % 8)), so that a store covers whole lines: straight from a thread's own
       // row it would touch 32 of them.
@@ -897,49 +939,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           whole ? reinterpret_cast<unsigned char*>(p.out)
                 : reinterpret_cast<unsigned char*>(
                       SHARED && d.j0 == 0
-                          ? w.first + (d.prefix ? 0 : (int64_t)p.B * Hq) * kRowF<D>
+                          ? w.first
                           : w.part + ((int64_t)d.slot * 2 * kTile + t * kTile) * kRowF<D>);
       const int64_t row_at = whole ? orow * D * 2
                              : (SHARED && d.j0 == 0 ? orow : (int64_t)row) * kRowF<D> * 4;
-      const uint32_t stage = (!narrow                ? base + 2 * C::TILE
-                              : is_small(d.n_tok) ? q_smem + C::HALVES * C::Q_SMALL
-                                                  : q_smem) +
-                             warp * kStage;
+      const uint32_t stage = kv_smem + C::STAGES * C::TILE + warp * kStage;
       const int passes = whole ? D / 64 : D / 32;
-      // 32 dims of the row from dim `at`, joined where there are two parts
-      auto result = [&](int at, uint32_t (&o)[2][16]) {
+#pragma unroll 1
+      for (int i = 0; i < passes; ++i) {
+        uint32_t o[2][16];
         if (d.j0 < d.j1) {
-          umma::tmem_ld16_async(tm_o + at, o[0]);
-          umma::tmem_ld16_async(tm_o + at + 16, o[1]);
+          const uint32_t src = tm_o + (whole ? 64 : 32) * i;
+          umma::tmem_ld16_async(src, o[0]);
+          umma::tmem_ld16_async(src + 16, o[1]);
           umma::tmem_wait_ld();
           umma::tmem_landed(o[0]);
           umma::tmem_landed(o[1]);
-          if (odd) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t x[16];
-              umma::tmem_ld16_async(tm_o + D + at + 16 * i, x);
-              umma::tmem_wait_ld();
-              umma::tmem_landed(x);
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                o[i][e] = __float_as_uint(
-                    fmaf(__uint_as_float(o[i][e]), f0, __uint_as_float(x[e]) * f1));
-            }
-          }
         }
         if (!(l > 0.0f)) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e >> 4][e & 15] = 0u;
         }
-      };
-#pragma unroll 1
-      for (int i = 0; i < passes; ++i) {
-        uint32_t o[2][16];
-        if (whole) {
-#pragma unroll 1
+        if (whole) {  // dims 64 i .. 64 i + 31, then the 32 behind them
+#pragma unroll
           for (int part = 0; part < 2; ++part) {
-            result(64 * i + 32 * part, o);
+            if (part) {
+              if (d.j0 < d.j1) {
+                umma::tmem_ld16_async(tm_o + 64 * i + 32, o[0]);
+                umma::tmem_ld16_async(tm_o + 64 * i + 48, o[1]);
+                umma::tmem_wait_ld();
+                umma::tmem_landed(o[0]);
+                umma::tmem_landed(o[1]);
+              }
+              if (!(l > 0.0f)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e >> 4][e & 15] = 0u;
+              }
+            }
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
               uint32_t v[4];
@@ -952,17 +988,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          result(32 * i, o);
 #pragma unroll
           for (int q8 = 0; q8 < 8; ++q8)
             st_shared16(stage + lane * 128 + ((q8 ^ (lane & 7)) << 4),
                         o[q8 >> 2][4 * (q8 & 3)], o[q8 >> 2][4 * (q8 & 3) + 1],
                         o[q8 >> 2][4 * (q8 & 3) + 2], o[q8 >> 2][4 * (q8 & 3) + 3]);
-        }
-        if (odd && i == passes - 1) {  // O_1 has been read
-          umma::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) umma::mbar_arrive(smem_u32(&sh.back[warp & 3]));
         }
         __syncwarp();
 #pragma unroll
@@ -979,11 +1009,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float2*>(base_out + row_at + D * 4) = make_float2(mc, l);
         else if (p.lse)
           p.lse[orow] = l > 0.0f ? mc * kLn2 + logf(l) : -INFINITY;
-      }
-      if (narrow && d.j0 < d.j1) {  // (the copy of the next Q is another proxy's write)
-        umma::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) umma::mbar_arrive(smem_u32(&sh.out_done[(n_item - 1) & 1]));
       }
     }
   }
@@ -1063,8 +1088,8 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
     join_rows_kernel(const AttendParams p, const Work w, int ctas) {
   const int units = p.n_groups + p.B;
-  const int64_t wide = w.line[units], thin = w.line[units + 1];
-  if (wide < 0) return;
+  const int64_t total = w.line[units], pages = w.line[units + 1];
+  if (total < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hq = p.Hkv * p.G, tpt = kTile / p.G;
   const int64_t orow = (int64_t)blockIdx.x * kJoinRows + warp;
@@ -1075,31 +1100,39 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (g < 0) return;
   const Unit own = load_unit<true>(p, p.n_groups + b);
   Join<D> a;
-  const int split = first_narrow(wide, thin, ctas);
-#pragma unroll 1
-  for (int part = 0; part < 2 && !own.bad; ++part) {
-    const int u = part ? p.n_groups + b : g;
-    const Unit un = part ? own : load_unit<true>(p, g);
-    if (un.n == 0) continue;
-    const int64_t total = un.narrow ? thin : wide;
-    const int cta0 = un.narrow ? split : 0;
-    const int n_cta = share_count(total, un.narrow ? ctas - split : split);
+  const int split = first_own(total, pages, ctas), g_row = hq - h * p.G;
+  const Unit un = load_unit<true>(p, g);
+  if (!own.bad && un.n > 0) {  // the pieces of the group's prefix
     const int t = (b - un.tok0) / (2 * tpt), i = (b - un.tok0) - t * 2 * tpt;
-    const int r = i / tpt * kTile + i % tpt * p.G + (hq - h * p.G);  // the row within the item
+    const int r = i / tpt * kTile + i % tpt * p.G + g_row;  // the row within the item
     const int64_t cost = item_cost(un, tpt, t);
-    const int64_t pos = w.line[u] + h * cost_before(un, tpt, unit_items(un, tpt)) +
+    const int64_t pos = w.line[g] + h * cost_before(un, tpt, unit_items(un, tpt)) +
                         cost_before(un, tpt, t);
     const int wt = item_weight(un, tpt, t);
     const int tiles = (item_keys(un, tpt, t) + kKeys - 1) / kKeys;
-    if (tiles == 0) continue;
-    for (int c = share_of(total, n_cta, pos); c < n_cta; ++c) {
-      const int64_t x0 = share_begin(total, n_cta, c), x1 = share_begin(total, n_cta, c + 1);
+    const int n = share_count(total, split, kMinShare);
+    for (int c = share_of(total, n, pos); c < n; ++c) {
+      const int64_t x0 = share_begin(total, n, c), x1 = share_begin(total, n, c + 1);
       if (x0 >= pos + cost) break;
       const int j0 = cut_tile(x0 - pos, cost, wt, tiles), j1 = cut_tile(x1 - pos, cost, wt, tiles);
-      if (j0 >= j1) continue;
-      a.add(j0 == 0 ? w.first + ((part ? (int64_t)p.B * Hq : 0) + orow) * kRowF<D>
-                    : w.part + ((int64_t)(cta0 + c) * 2 * kTile + r) * kRowF<D>,
-            lane);
+      if (j0 < j1)
+        a.add(j0 == 0 ? w.first + orow * kRowF<D>
+                      : w.part + ((int64_t)c * 2 * kTile + r) * kRowF<D>,
+              lane);
+    }
+  }
+  if (!own.bad && own.kv_len > 0) {  // and those of its own pages
+    const int n_pages = own_pages(own);
+    const int64_t cost = own_cost(own), pos = w.line[p.n_groups + b] + h * cost;
+    const int n = share_count(pages, (ctas - split) * kWarps, kMinPages);
+    for (int c = share_of(pages, n, pos); c < n; ++c) {
+      const int64_t x0 = share_begin(pages, n, c), x1 = share_begin(pages, n, c + 1);
+      if (x0 >= pos + cost) break;
+      const int i0 = own_cut(x0 - pos, n_pages), i1 = own_cut(x1 - pos, n_pages);
+      if (i0 < i1)
+        a.add(i0 == 0 ? w.first + ((int64_t)p.B * Hq + orow) * kRowF<D>
+                      : w.own + ((int64_t)c * 8 + g_row) * kRowF<D>,
+              lane);
     }
   }
   a.write(p.out, p.lse, orow, lane);
@@ -1123,6 +1156,7 @@ size_t lay_out(const AttendParams& p, int ctas, void* ws, Work* w) {
   x.head = reinterpret_cast<Head*>(take(shared ? 0 : 2 * sizeof(Head) * ctas));
   x.part = reinterpret_cast<float*>(take((size_t)(shared ? 1 : 2) * ctas * 2 * kTile * row));
   x.first = reinterpret_cast<float*>(take(shared ? 2 * (size_t)p.B * p.Hkv * p.G * row : 0));
+  x.own = reinterpret_cast<float*>(take(shared ? (size_t)ctas * kWarps * 8 * row : 0));
   x.line = reinterpret_cast<int64_t*>(take(shared ? ((size_t)p.n_groups + p.B + 2) * 8 : 0));
   if (w) *w = x;
   return at;
@@ -1166,19 +1200,19 @@ bool encode(CUtensorMap* m, const void* base, int rank, const int64_t* dims, con
 template <int D, bool SHARED>
 cudaError_t launch(const AttendParams& p, const Work& w, int ctas, cudaStream_t s) {
   const int tpt = kTile / p.G;
-  CUtensorMap q, q1, k, v;
+  CUtensorMap q, k, v;
   const int64_t qd[3] = {D, (int64_t)p.Hkv * p.G, p.T}, qs[2] = {D, p.sq_t};
-  const int qb[3] = {64, p.G, tpt}, qb1[3] = {64, p.G, kSmall / p.G};
+  const int qb[3] = {64, p.G, tpt};
   const int64_t kd[4] = {D, kPage, p.Hkv, p.kv.num_pages};
   const int64_t ks[3] = {p.kv.sk_t, p.kv.sk_h, p.kv.sk_p}, vs[3] = {p.kv.sv_t, p.kv.sv_h, p.kv.sv_p};
   const int kb[4] = {64, kPage, 1, 1};
-  if (!encode_fn() || !encode(&q, p.q, 3, qd, qs, qb) || !encode(&q1, p.q, 3, qd, qs, qb1) ||
+  if (!encode_fn() || !encode(&q, p.q, 3, qd, qs, qb) ||
       !encode(&k, p.kv.k_pool, 4, kd, ks, kb) || !encode(&v, p.kv.v_pool, 4, kd, vs, kb))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, SHARED>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
-  attend_kernel<D, SHARED><<<ctas, kThreads, Cfg<D>::SMEM, s>>>(p, w, q, q1, k, v);
+  attend_kernel<D, SHARED><<<ctas, kThreads, Cfg<D>::SMEM, s>>>(p, w, q, k, v);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (SHARED) {

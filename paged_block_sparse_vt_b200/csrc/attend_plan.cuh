@@ -8,10 +8,9 @@
 // tile and both neighbours compute it alike, so every tile has one owner, every CTA ends within
 // a tile's cost of the others, and a CTA has at most one item that began before it.
 //
-// There are two such lines, and the CTAs are dealt between them by their lengths.  Units of one
-// row tile (decode, drafted tokens, a prefix that few share) read their keys once for few rows:
-// they are bound by bytes, what they need is many of those in flight, and nearly all shared memory
-// of their CTAs goes to them.  All others need room for two tiles of queries and for results.
+// What a single token attends to by itself (a decode row's own pages) is too little work for a
+// row tile and bound by the bytes of its keys: it stands in a second line, in pages, that is cut
+// into one share per warp.  The CTAs are dealt between the two lines by their lengths.
 #pragma once
 
 #include <stdint.h>
@@ -21,12 +20,22 @@ namespace vt {
 constexpr int kTile = 128;  // query rows of one accumulator tile; an item has two
 constexpr int kKeys = 128;  // keys of one step
 
-// Costs, in keys times a weight.  An item of one row tile takes less than one of two, but not
-// half: its keys are loaded all the same.
-constexpr int kCostTwo = 4, kCostOne = 3, kCostNarrow = 3;
+// Costs, in keys times a weight.  An item of one row tile takes as long as one of two: nothing
+// runs beside its chain of scores, softmax and values (a step of 128 keys: 3.7 k cycles, and of
+// two row tiles 3.5 k).
+constexpr int kCostTwo = 4, kCostOne = 4;
 constexpr int kCostItem = 256;      // loading q, filling the pipeline, writing out
-constexpr int kCostItemNarrow = 128;
 constexpr int64_t kMinShare = 4 * kKeys * kCostTwo;  // no CTA takes less than four key tiles
+
+// The second line: pages of a request's own, for each KV head, and what an item of them costs
+// beyond (its query, its result).
+constexpr int kWarps = 12;        // of a CTA, each with a share
+constexpr int kOwnItem = 2;       // pages
+constexpr int kMinPages = 4;      // no warp takes less
+// A page of one head in the costs of the first line, measured: 256 requests on one prefix of 65536
+// tokens took 791 us with 20, 639 with 35, 565 with 50, 552 with 70; 128 requests with long own
+// parts 176, 184, 185, 215.
+constexpr int kOwnPage = 50;
 
 struct Unit {
   int tok0, n;     // its query tokens (0: no items)
@@ -35,10 +44,14 @@ struct Unit {
   int kv_len;      // keys there are, from page `page0` of table row `row`
   int page0, row;
   bool bad;        // a bad length: no keys, empty rows
-  bool narrow;
 };
 
 #define VT_HD __host__ __device__ __forceinline__
+
+// A decode row's own pages, and the cost of one head's item of them in the second line.
+VT_HD int own_pages(const Unit& u) { return (u.kv_len + 15) / 16; }
+VT_HD int64_t own_cost(const Unit& u) { return u.kv_len > 0 ? own_pages(u) + kOwnItem : 0; }
+VT_HD int own_cut(int64_t x, int pages) { return x <= 0 ? 0 : x < pages ? (int)x : pages; }
 
 // Items of one head; tpt: tokens of a row tile.
 VT_HD int unit_items(const Unit& u, int tpt) { return (u.n + 2 * tpt - 1) / (2 * tpt); }
@@ -51,12 +64,11 @@ VT_HD int item_keys(const Unit& u, int tpt, int t) {
 }
 
 VT_HD int item_weight(const Unit& u, int tpt, int t) {
-  return u.narrow ? kCostNarrow : u.n - t * 2 * tpt > tpt ? kCostTwo : kCostOne;
+  return u.n - t * 2 * tpt > tpt ? kCostTwo : kCostOne;
 }
 
 VT_HD int64_t item_cost(const Unit& u, int tpt, int t) {
-  return (int64_t)item_weight(u, tpt, t) *
-         ((u.narrow ? kCostItemNarrow : kCostItem) + item_keys(u, tpt, t));
+  return (int64_t)item_weight(u, tpt, t) * (kCostItem + item_keys(u, tpt, t));
 }
 
 // Cost of a head's items before t <= unit_items; all but the last item have two full tiles.
@@ -78,18 +90,20 @@ VT_HD int cut_tile(int64_t x, int64_t cost, int weight, int n_tiles) {
   return t < n_tiles ? (int)t : n_tiles;
 }
 
-// The CTAs from which on the narrow line is worked on.
-VT_HD int first_narrow(int64_t wide, int64_t narrow, int ctas) {
-  if (narrow == 0) return ctas;
-  if (wide == 0) return 0;
-  const int n = (int)((double)narrow / (double)(wide + narrow) * ctas + 0.5);
+// The CTA from which on the second line is worked on; `tiles` and `pages`: the lines' lengths.
+VT_HD int first_own(int64_t tiles, int64_t pages, int ctas) {
+  if (pages == 0) return ctas;
+  if (tiles == 0) return 0;
+  const double own = (double)pages * kOwnPage;
+  const int n = (int)(own / ((double)tiles + own) * ctas + 0.5);
   return ctas - (n < 1 ? 1 : n > ctas - 1 ? ctas - 1 : n);
 }
 
-// CTAs that share a line of length `total`, and where the c-th share begins.
-VT_HD int share_count(int64_t total, int ctas) {
-  const int64_t n = total / kMinShare;
-  return n < 1 ? 1 : n < ctas ? (int)n : ctas;
+// Those (of `most`) that share a line of length `total`, no share less than `least`, and where
+// the c-th share begins.
+VT_HD int share_count(int64_t total, int most, int64_t least) {
+  const int64_t n = total / least;
+  return n < 1 ? 1 : n < most ? (int)n : most;
 }
 VT_HD int64_t share_begin(int64_t total, int n, int c) {
   return total / n * c + total % n * c / n;

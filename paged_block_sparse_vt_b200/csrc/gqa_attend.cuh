@@ -68,13 +68,14 @@ struct WarpAttention {
   int g, qd;
   uint32_t koff, voff;
 
-  // q_rows: the G query rows of the unit (bf16 [G][D], 4-byte aligned)
-  __device__ __forceinline__ void init(const __nv_bfloat16* q_rows, int lane) {
+  // q_rows: the G query rows of the unit (bf16 [G][D], 4-byte aligned), or the `heads` <= G first
+  // of them, where that is known only at run time
+  __device__ __forceinline__ void init(const __nv_bfloat16* q_rows, int lane, int heads = G) {
     g = lane >> 2;
     qd = 2 * (lane & 3);
 #pragma unroll
     for (int ks = 0; ks < T::KS; ++ks) {
-      if (g < G) {
+      if (g < heads) {
         const __nv_bfloat16* qr = q_rows + (int64_t)g * D + ks * 16 + qd;
         qa0[ks] = *reinterpret_cast<const uint32_t*>(qr);
         qa2[ks] = *reinterpret_cast<const uint32_t*>(qr + 8);
@@ -90,8 +91,12 @@ struct WarpAttention {
     voff = (((lane & 7) + ((lane >> 3) & 1) * 8) * T::ROW + (lane >> 4) * 8) * 2;
   }
 
-  // Attend to one staged page with vr valid tokens; qscale = sm_scale * log2(e).
+  // Attend to one staged page with vr valid tokens; qscale = sm_scale * log2(e).  ROUNDED: the sum
+  // takes the weights as the MMA does, else as they were before they were rounded (then the lse
+  // is good to fp32, and the rounding stays out of the normaliser).
+  template <bool ROUNDED = true>
   __device__ __forceinline__ void page(uint32_t slot, int vr, float qscale) {
+    auto bf16_round = [](float x) { return ROUNDED ? vt::bf16_round(x) : x; };
     const uint32_t kt = slot, vt = slot + T::TILE;
     float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
