@@ -431,85 +431,154 @@ def vt_plan_requests(seq_lens: torch.Tensor, order: Optional[torch.Tensor] = Non
     return order
 
 
-def _same_device(first: torch.Tensor, where: str, *others: Optional[torch.Tensor]) -> None:
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise VtError(VT_ERR_INVALID_ARG, where, "tensors on different devices")
+# ---- dense attention and page calls -----------------------------------------------------------
+# These run once per layer and step, often on little work, so their checks are written flat: one
+# test per tensor, and the words for a failure only when there is one.
+
+_current_device = torch._C._cuda_getDevice
 
 
-def _table(page_table: torch.Tensor) -> None:
-    _need(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2 or page_table.stride(1) != 1:
-        raise VtError(VT_ERR_INVALID_ARG, "page_table", "must be [B, max_pages] with unit inner stride")
+def _fail(t, name: str, dtype, dev: int, contiguous: bool = True):
+    _need(t, name, dtype, contiguous=contiguous)
+    raise VtError(VT_ERR_INVALID_ARG, name, f"on {t.device}, not on device {dev}")
+
+
+def _vec(t, name: str, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of this type on device ``dev``."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev \
+            or not t.is_contiguous():
+        _fail(t, name, dtype, dev)
+    return t.data_ptr()
 
 
 def _sized(t: torch.Tensor, name: str, shape: tuple) -> None:
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise VtError(VT_ERR_INVALID_ARG, name, f"must be {list(shape)}, got {list(t.shape)}")
 
 
-def _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, status):
+def _table(page_table: torch.Tensor, dev: int):
+    """(rows, row stride) of a page table."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32 \
+            or page_table.get_device() != dev:
+        _fail(page_table, "page_table", torch.int32, dev, contiguous=False)
+    if page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise VtError(VT_ERR_INVALID_ARG, "page_table", "must be [B, max_pages] with unit inner stride")
+    rows, width = page_table.shape
+    return rows, page_table.stride(0) if rows > 1 else width
+
+
+def _pools(k_pool, v_pool, dev: int) -> PagedKV:
     kv = paged_kv(k_pool, v_pool)
-    _need(q, "q", torch.bfloat16)
-    _table(page_table)
-    _need(seq_lens, "seq_lens", torch.int32, contiguous=True)
-    _need(q_start, "q_start", torch.int32, contiguous=True)
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _same_device(q, "vt_prefill", k_pool, v_pool, page_table, seq_lens, q_start, status)
-    B = page_table.shape[0]
+    if k_pool.get_device() != dev or v_pool.get_device() != dev:
+        _fail(k_pool, "k_pool", torch.bfloat16, dev, contiguous=False)
+    if v_pool.shape[:3] != k_pool.shape[:3]:
+        raise VtError(VT_ERR_INVALID_ARG, "pools", "K and V pools of different shapes")
+    return kv
+
+
+def _status(status, dev: int):
+    if status is None:
+        return None
+    if not isinstance(status, torch.Tensor) or status.dtype is not torch.int32 \
+            or status.get_device() != dev:
+        _fail(status, "status", torch.int32, dev, contiguous=False)
+    return status.data_ptr()
+
+
+def _gpu(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise VtError(VT_ERR_INVALID_ARG, name, "must be a CUDA tensor")
+    return t.get_device()
+
+
+def _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, status):
+    dev = _gpu(q, "q")
+    kv = _pools(k_pool, v_pool, dev)
+    B, pt_stride = _table(page_table, dev)
+    if q.dtype is not torch.bfloat16:
+        _need(q, "q", torch.bfloat16)
     if q.dim() != 3 or q.shape[2] != kv.head_dim:
         raise VtError(VT_ERR_INVALID_ARG, "q", f"must be [T, Hq, {kv.head_dim}]")
     T, hq, d = q.shape
-    if q.stride(2) != 1 or (hq > 1 and q.stride(1) != d):
+    st, sh, sd = q.stride()
+    if sd != 1 or (hq > 1 and sh != d):
         raise VtError(VT_ERR_INVALID_ARG, "q", "a token's heads must be contiguous")
+    seq = _vec(seq_lens, "seq_lens", torch.int32, dev)
+    start = _vec(q_start, "q_start", torch.int32, dev)
     _sized(seq_lens, "seq_lens", (B,))
     _sized(q_start, "q_start", (B + 1,))
-    a = PrefillArgs(B, hq, T, q.data_ptr(), q.stride(0) if T > 1 else hq * d, q_start.data_ptr(),
-                    page_table.data_ptr(), page_table.stride(0) if B > 1 else page_table.shape[1],
-                    seq_lens.data_ptr(), float(sm_scale), _ptr(status))
-    return kv, a
+    return kv, PrefillArgs(B, hq, T, q.data_ptr(), st if T > 1 else hq * d, start,
+                           page_table.data_ptr(), pt_stride, seq, float(sm_scale),
+                           _status(status, dev))
 
 
 def _attend_outputs(q, out, lse, want_lse):
+    dev, shape = q.get_device(), q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    _need(out, "out", torch.bfloat16, contiguous=True)
-    _sized(out, "out", tuple(q.shape))
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    else:
+        _vec(out, "out", torch.bfloat16, dev)
+        _sized(out, "out", shape)
     if lse is not None:
-        _need(lse, "lse", torch.float32, contiguous=True)
-        _sized(lse, "lse", tuple(q.shape[:2]))
-    _same_device(q, "out/lse", out, lse)
+        _vec(lse, "lse", torch.float32, dev)
+        _sized(lse, "lse", shape[:2])
+    elif want_lse:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
     return out, lse
 
 
-def _workspace(need: int, workspace, device):
-    """The given workspace, or a new one of ``need`` bytes (any contents)."""
+def _workspace(workspace, need: int, dev: int):
+    """(tensor, address, bytes) of the given workspace, or of a new one (any contents)."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _need(workspace, "workspace", torch.uint8, contiguous=True)
-    if workspace.device != device:
-        raise VtError(VT_ERR_INVALID_ARG, "workspace", "on another device")
-    return workspace
+        workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}") if need else None
+        return workspace, _ptr(workspace), need
+    return workspace, _vec(workspace, "workspace", torch.uint8, dev), workspace.numel()
 
 
-def _device_call(fn, where: str, t: torch.Tensor, *args):
-    """fn(*args, stream) with t's device current (kernels run where their tensors are)."""
-    if torch.cuda.current_device() == t.get_device():
-        _check(fn(*args, _stream(t)), where)
+# Bytes of workspace by what they depend on beside the device: a few shapes in a program's life.
+_ws_bytes: dict = {}
+
+
+def _ws_size(key: tuple, size_of) -> int:
+    n = _ws_bytes.get(key)
+    if n is None:
+        n = int(size_of())
+        if n:  # 0: the call has nothing to do, or will say what is wrong
+            if len(_ws_bytes) >= 4096:
+                _ws_bytes.clear()
+            _ws_bytes[key] = n
+    return n
+
+
+def _device_call(fn, where: str, dev: int, *args) -> None:
+    """fn(*args, stream) with device ``dev`` current (kernels run where their tensors are)."""
+    if _current_device() == dev:
+        rc = fn(*args, _raw_stream(dev) if _raw_stream is not None
+                else torch.cuda.current_stream(dev).cuda_stream)
     else:
-        with torch.cuda.device(t.device):
-            _check(fn(*args, _stream(t)), where)
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != VT_OK:
+        _check(rc, where)
+
+
+def _prefill_ws(lib, dev: int, kv: PagedKV, a: PrefillArgs) -> int:
+    if a.batch == 0 or a.num_tokens == 0:
+        return 0
+    return _ws_size(("prefill", dev, kv.head_dim), lambda: _on_device(
+        dev, lib.vt_prefill_workspace_size, ctypes.byref(kv), ctypes.byref(a)))
+
+
+def _on_device(dev: int, fn, *args):
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def prefill_workspace(q, k_pool, v_pool, page_table, seq_lens, q_start) -> Optional[torch.Tensor]:
     """A workspace for vt_prefill with these shapes (any contents; None when none is needed)."""
-    lib = load_library()
     kv, a = _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, 1.0, None)
-    return _workspace(int(lib.vt_prefill_workspace_size(ctypes.byref(kv), ctypes.byref(a))), None,
-                      q.device)
+    dev = q.get_device()
+    return _workspace(None, _prefill_ws(load_library(), dev, kv, a), dev)[0]
 
 
 def vt_prefill(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, out=None, lse=None,
@@ -522,48 +591,47 @@ def vt_prefill(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, out=N
     """
     lib = load_library()
     kv, a = _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, status)
+    dev = q.get_device()
     out, lse = _attend_outputs(q, out, lse, want_lse)
-    need = int(lib.vt_prefill_workspace_size(ctypes.byref(kv), ctypes.byref(a)))
-    workspace = _workspace(need, workspace, q.device)
-    _device_call(lib.vt_prefill, "vt_prefill", q, ctypes.byref(kv), ctypes.byref(a),
-                 out.data_ptr(), _ptr(lse), _ptr(workspace),
-                 0 if workspace is None else workspace.numel())
+    workspace, ws, ws_bytes = _workspace(workspace, _prefill_ws(lib, dev, kv, a), dev)
+    _device_call(lib.vt_prefill, "vt_prefill", dev, kv, a, out.data_ptr(), _ptr(lse), ws, ws_bytes)
     return out, lse
 
 
 def _shared_args(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pages, sm_scale,
                  status):
-    kv = paged_kv(k_pool, v_pool)
-    _need(q, "q", torch.bfloat16, contiguous=True)
-    _table(page_table)
-    _need(seq_lens, "seq_lens", torch.int32, contiguous=True)
-    _need(group_start, "group_start", torch.int32, contiguous=True)
-    _need(prefix_pages, "prefix_pages", torch.int32, contiguous=True)
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _same_device(q, "vt_shared_prefix_decode", k_pool, v_pool, page_table, seq_lens, group_start,
-                 prefix_pages, status)
-    B, groups = page_table.shape[0], prefix_pages.numel()
+    dev = _gpu(q, "q")
+    kv = _pools(k_pool, v_pool, dev)
+    B, pt_stride = _table(page_table, dev)
+    qp = _vec(q, "q", torch.bfloat16, dev)
     if q.dim() != 3 or q.shape[0] != B or q.shape[2] != kv.head_dim:
         raise VtError(VT_ERR_INVALID_ARG, "q", f"must be [{B}, Hq, {kv.head_dim}]")
+    seq = _vec(seq_lens, "seq_lens", torch.int32, dev)
+    start = _vec(group_start, "group_start", torch.int32, dev)
+    prefix = _vec(prefix_pages, "prefix_pages", torch.int32, dev)
+    groups = prefix_pages.numel()
     _sized(seq_lens, "seq_lens", (B,))
     _sized(group_start, "group_start", (groups + 1,))
     _sized(prefix_pages, "prefix_pages", (groups,))
-    a = SharedPrefixArgs(B, q.shape[1], groups, q.data_ptr(), group_start.data_ptr(),
-                         prefix_pages.data_ptr(), page_table.data_ptr(),
-                         page_table.stride(0) if B > 1 else page_table.shape[1],
-                         seq_lens.data_ptr(), float(sm_scale), _ptr(status))
-    return kv, a
+    return kv, SharedPrefixArgs(B, q.shape[1], groups, qp, start, prefix, page_table.data_ptr(),
+                                pt_stride, seq, float(sm_scale), _status(status, dev))
+
+
+def _shared_ws(lib, dev: int, kv: PagedKV, a: SharedPrefixArgs) -> int:
+    if a.batch == 0 or a.num_groups == 0:
+        return 0
+    return _ws_size(("shared", dev, kv.head_dim, a.batch, a.num_q_heads, a.num_groups),
+                    lambda: _on_device(dev, lib.vt_shared_prefix_workspace_size, ctypes.byref(kv),
+                                       ctypes.byref(a)))
 
 
 def shared_prefix_workspace(q, k_pool, v_pool, page_table, seq_lens, group_start,
                             prefix_pages) -> Optional[torch.Tensor]:
     """A workspace for vt_shared_prefix_decode with these shapes (any contents)."""
-    lib = load_library()
     kv, a = _shared_args(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pages, 1.0,
                          None)
-    return _workspace(int(lib.vt_shared_prefix_workspace_size(ctypes.byref(kv), ctypes.byref(a))),
-                      None, q.device)
+    dev = q.get_device()
+    return _workspace(None, _shared_ws(load_library(), dev, kv, a), dev)[0]
 
 
 def vt_shared_prefix_decode(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pages,
@@ -578,57 +646,53 @@ def vt_shared_prefix_decode(q, k_pool, v_pool, page_table, seq_lens, group_start
     lib = load_library()
     kv, a = _shared_args(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pages,
                          sm_scale, status)
+    dev = q.get_device()
     out, lse = _attend_outputs(q, out, lse, want_lse)
-    need = int(lib.vt_shared_prefix_workspace_size(ctypes.byref(kv), ctypes.byref(a)))
-    workspace = _workspace(need, workspace, q.device)
-    _device_call(lib.vt_shared_prefix_decode, "vt_shared_prefix_decode", q, ctypes.byref(kv),
-                 ctypes.byref(a), out.data_ptr(), _ptr(lse), _ptr(workspace),
-                 0 if workspace is None else workspace.numel())
+    workspace, ws, ws_bytes = _workspace(workspace, _shared_ws(lib, dev, kv, a), dev)
+    _device_call(lib.vt_shared_prefix_decode, "vt_shared_prefix_decode", dev, kv, a,
+                 out.data_ptr(), _ptr(lse), ws, ws_bytes)
     return out, lse
 
 
-def _books(page_table, seq_lens, refs, status, *lists) -> PageBooks:
-    _table(page_table)
-    _need(seq_lens, "seq_lens", torch.int32, contiguous=True)
-    _need(refs, "refs", torch.int32, contiguous=True)
-    _sized(seq_lens, "seq_lens", (page_table.shape[0],))
-    if status is not None:
-        _need(status, "status", torch.int32)
-    for t in lists:
-        _need(t, "list of requests", torch.int32, contiguous=True)
-        _sized(t, "list of requests", (lists[0].numel(),))
-    _same_device(page_table, "page books", seq_lens, refs, status, *lists)
-    R, width = page_table.shape
-    return PageBooks(R, page_table.data_ptr(), page_table.stride(0) if R > 1 else width,
-                     seq_lens.data_ptr(), refs.data_ptr(), _ptr(status))
+def _books(page_table, seq_lens, refs, status, dev: int) -> PageBooks:
+    rows, pt_stride = _table(page_table, dev)
+    seq = _vec(seq_lens, "seq_lens", torch.int32, dev)
+    _sized(seq_lens, "seq_lens", (rows,))
+    return PageBooks(rows, page_table.data_ptr(), pt_stride, seq,
+                     _vec(refs, "refs", torch.int32, dev), _status(status, dev))
 
 
-def _pool_pages(k_pool, v_pool, refs, centroids) -> PagedKV:
-    kv = paged_kv(k_pool, v_pool)
-    if v_pool.shape[:3] != k_pool.shape[:3]:
-        raise VtError(VT_ERR_INVALID_ARG, "pools", "K and V pools of different shapes")
-    if refs is not None:
-        _sized(refs, "refs", (k_pool.shape[0],))
-    if centroids is not None:
-        _need(centroids, "centroids", torch.float32, contiguous=True)
-        _sized(centroids, "centroids", (k_pool.shape[0], k_pool.shape[2], k_pool.shape[3]))
-    _same_device(k_pool, "pools", v_pool, refs, centroids)
-    return kv
+def _lists(dev: int, first, second, names: tuple):
+    """(length, addresses) of one or two lists of equal length."""
+    a = _vec(first, names[0], torch.int32, dev)
+    if second is None:
+        return first.numel(), a, None
+    b = _vec(second, names[1], torch.int32, dev)
+    if second.shape != first.shape:
+        raise VtError(VT_ERR_INVALID_ARG, names[1], f"must be {list(first.shape)}, got "
+                                                    f"{list(second.shape)}")
+    return first.numel(), a, b
+
+
+def _pool_books(k_pool, v_pool, refs, centroids, dev: int):
+    kv = _pools(k_pool, v_pool, dev)
+    if refs is not None and (not isinstance(refs, torch.Tensor) or refs.numel() != kv.num_pages):
+        raise VtError(VT_ERR_INVALID_ARG, "refs", f"must be [{kv.num_pages}]")
+    if centroids is None:
+        return kv, None
+    cent = _vec(centroids, "centroids", torch.float32, dev)
+    _sized(centroids, "centroids", (kv.num_pages, kv.num_kv_heads, kv.head_dim))
+    return kv, cent
 
 
 def vt_copy_pages(k_pool, v_pool, src, dst, centroids=None, status=None) -> None:
     """Pages dst[i] become copies of pages src[i] (K, V and, where given, centroid rows); no page
     may be listed twice in ``dst``, or in both lists.  One pool as both K and V is copied once."""
     lib = load_library()
-    kv = _pool_pages(k_pool, v_pool, None, centroids)
-    for t, name in ((src, "src"), (dst, "dst")):
-        _need(t, name, torch.int32, contiguous=True)
-    _sized(dst, "dst", tuple(src.shape))
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _same_device(k_pool, "vt_copy_pages", src, dst, status)
-    _device_call(lib.vt_copy_pages, "vt_copy_pages", k_pool, ctypes.byref(kv), src.data_ptr(),
-                 dst.data_ptr(), src.numel(), _ptr(centroids), _ptr(status))
+    dev = _gpu(k_pool, "k_pool")
+    kv, cent = _pool_books(k_pool, v_pool, None, centroids, dev)
+    n, a, b = _lists(dev, src, dst, ("src", "dst"))
+    _device_call(lib.vt_copy_pages, "vt_copy_pages", dev, kv, a, b, n, cent, _status(status, dev))
 
 
 def page_workspace(num_pages: int, n: int, device) -> torch.Tensor:
@@ -637,19 +701,23 @@ def page_workspace(num_pages: int, n: int, device) -> torch.Tensor:
                        dtype=torch.uint8, device=device)
 
 
+def _page_ws(lib, workspace, pages: int, n: int, dev: int):
+    need = _ws_size(("pages", pages, n), lambda: lib.vt_page_workspace_size(pages, n)) \
+        if workspace is None else 0
+    return _workspace(workspace, need, dev)
+
+
 def vt_fork_requests(k_pool, v_pool, page_table, seq_lens, refs, parents, children, status=None,
                      workspace=None) -> None:
     """Rows children[i] become forks of rows parents[i]: full pages are shared, a partly filled
     last page is copied to a page of its own (the lowest free ones, in list order)."""
     lib = load_library()
-    kv = _pool_pages(k_pool, v_pool, refs, None)
-    books = _books(page_table, seq_lens, refs, status, parents, children)
-    _same_device(k_pool, "vt_fork_requests", page_table)
-    n = parents.numel()
-    workspace = _workspace(int(lib.vt_page_workspace_size(refs.numel(), n)), workspace, refs.device)
-    _device_call(lib.vt_fork_requests, "vt_fork_requests", refs, ctypes.byref(kv),
-                 ctypes.byref(books), parents.data_ptr(), children.data_ptr(), n,
-                 workspace.data_ptr(), workspace.numel())
+    dev = _gpu(k_pool, "k_pool")
+    kv, _ = _pool_books(k_pool, v_pool, refs, None, dev)
+    books = _books(page_table, seq_lens, refs, status, dev)
+    n, a, b = _lists(dev, parents, children, ("parents", "children"))
+    workspace, ws, ws_bytes = _page_ws(lib, workspace, kv.num_pages, n, dev)
+    _device_call(lib.vt_fork_requests, "vt_fork_requests", dev, kv, books, a, b, n, ws, ws_bytes)
 
 
 def vt_extend_requests(page_table, seq_lens, refs, requests, tokens, status=None,
@@ -657,20 +725,22 @@ def vt_extend_requests(page_table, seq_lens, refs, requests, tokens, status=None
     """Rows requests[i] grow by tokens[i] tokens; the pages that takes are appended (the lowest
     free ones, in list order).  A new request starts from a row of length 0."""
     lib = load_library()
-    books = _books(page_table, seq_lens, refs, status, requests, tokens)
-    n = requests.numel()
-    workspace = _workspace(int(lib.vt_page_workspace_size(refs.numel(), n)), workspace, refs.device)
-    _device_call(lib.vt_extend_requests, "vt_extend_requests", refs, ctypes.byref(books),
-                 refs.numel(), requests.data_ptr(), tokens.data_ptr(), n,
-                 _ptr(workspace), 0 if workspace is None else workspace.numel())
+    dev = _gpu(refs, "refs")
+    books = _books(page_table, seq_lens, refs, status, dev)
+    n, a, b = _lists(dev, requests, tokens, ("requests", "tokens"))
+    pages = refs.numel()
+    workspace, ws, ws_bytes = _page_ws(lib, workspace, pages, n, dev)
+    _device_call(lib.vt_extend_requests, "vt_extend_requests", dev, books, pages, a, b, n, ws,
+                 ws_bytes)
 
 
 def vt_free_requests(page_table, seq_lens, refs, requests, status=None) -> None:
     """Rows requests[i] end: their pages lose a reference, their lengths become 0."""
     lib = load_library()
-    books = _books(page_table, seq_lens, refs, status, requests)
-    _device_call(lib.vt_free_requests, "vt_free_requests", refs, ctypes.byref(books), refs.numel(),
-                 requests.data_ptr(), requests.numel())
+    dev = _gpu(refs, "refs")
+    books = _books(page_table, seq_lens, refs, status, dev)
+    n, a, _ = _lists(dev, requests, None, ("requests",))
+    _device_call(lib.vt_free_requests, "vt_free_requests", dev, books, refs.numel(), a, n)
 
 
 def vt_compact_pages(k_pool, v_pool, page_table, seq_lens, refs, centroids=None, n_used=None,
@@ -678,16 +748,14 @@ def vt_compact_pages(k_pool, v_pool, page_table, seq_lens, refs, centroids=None,
     """The used pages move to the front of the pools, tables and counts with them.  Returns
     n_used, int32 [1] on the device: pages n_used and up are free."""
     lib = load_library()
-    kv = _pool_pages(k_pool, v_pool, refs, centroids)
-    books = _books(page_table, seq_lens, refs, status)
-    _same_device(k_pool, "vt_compact_pages", page_table, n_used)
+    dev = _gpu(k_pool, "k_pool")
+    kv, cent = _pool_books(k_pool, v_pool, refs, centroids, dev)
+    books = _books(page_table, seq_lens, refs, status, dev)
     if n_used is None:
         n_used = torch.empty(1, dtype=torch.int32, device=refs.device)
-    _need(n_used, "n_used", torch.int32)
-    workspace = _workspace(int(lib.vt_page_workspace_size(refs.numel(), 0)), workspace, refs.device)
-    _device_call(lib.vt_compact_pages, "vt_compact_pages", refs, ctypes.byref(kv),
-                 ctypes.byref(books), _ptr(centroids), n_used.data_ptr(), workspace.data_ptr(),
-                 workspace.numel())
+    workspace, ws, ws_bytes = _page_ws(lib, workspace, kv.num_pages, 0, dev)
+    _device_call(lib.vt_compact_pages, "vt_compact_pages", dev, kv, books, cent,
+                 _vec(n_used, "n_used", torch.int32, dev), ws, ws_bytes)
     return n_used
 
 

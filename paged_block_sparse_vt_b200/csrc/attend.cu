@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tpt = kTile / p.G;
   const int cta = blockIdx.x;
   volatile int* abort_flag = &sh.abort;
+  let_next_launch();
   // the cost tables of both lines lie where q comes later
   int64_t* table0 = reinterpret_cast<int64_t*>(raw + (base - smem_u32(raw)));
   int64_t* table1 = table0 + kPlan + 1;
@@ -1064,6 +1065,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
     join_items_kernel(const AttendParams p, const Work w) {
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_previous();
   const Head h0 = w.head[2 * c + 1];
   if (!h0.valid) return;
   const int tpt = kTile / p.G, Hq = p.Hkv * p.G;
@@ -1083,25 +1085,73 @@ __global__ void __launch_bounds__(kJoinThreads)
   a.write(p.out, p.lse, (int64_t)(h0.tok0 + tok) * Hq + h0.h * p.G + in % p.G, lane);
 }
 
-// Shared prefixes: a warp joins one row: the pieces of its group's prefix, and of its own pages.
+// Shared prefixes: a warp joins one row, the pieces of its group's prefix and of its own pages.
+// Which shares hold a piece is worked out for 32 of them at a time, a lane each, and their m and l
+// are read at once: one after the other, a prefix of 18 pieces took 18 trips to memory (23 us).
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
     join_rows_kernel(const AttendParams p, const Work w, int ctas) {
-  const int units = p.n_groups + p.B;
-  const int64_t total = w.line[units], pages = w.line[units + 1];
-  if (total < 0) return;
+  constexpr int E = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hq = p.Hkv * p.G, tpt = kTile / p.G;
   const int64_t orow = (int64_t)blockIdx.x * kJoinRows + warp;
   if (orow >= (int64_t)p.B * Hq) return;
   const int b = (int)(orow / Hq), hq = (int)(orow - (int64_t)b * Hq);
-  const int h = hq / p.G;
+  const int h = hq / p.G, g_row = hq - h * p.G;
+  const int units = p.n_groups + p.B;
+  wait_for_previous();
+  const int64_t total = w.line[units], pages = w.line[units + 1];
+  const int64_t own_line = w.line[p.n_groups + b];
+  if (total < 0) return;
   const int g = group_of(p, b);
   if (g < 0) return;
-  const Unit own = load_unit<true>(p, p.n_groups + b);
-  Join<D> a;
-  const int split = first_own(total, pages, ctas), g_row = hq - h * p.G;
-  const Unit un = load_unit<true>(p, g);
+  const Unit own = load_unit<true>(p, p.n_groups + b), un = load_unit<true>(p, g);
+  const int split = first_own(total, pages, ctas);
+  float o[E], m = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  // joins the pieces that the lanes name (NULL: none)
+  auto join = [&](const float* piece) {
+    const float2 ml = piece ? __ldcg(reinterpret_cast<const float2*>(piece + D))
+                            : make_float2(-INFINITY, 0.0f);
+    float top = fmaxf(m, ml.x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+    const float keep = m == -INFINITY ? 0.0f : exp2f(m - top);
+    const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+    float sum = ml.y * f;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
+    l = l * keep + sum;
+    m = top;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= keep;
+    for (uint32_t left = __ballot_sync(kFull, piece != nullptr); left;) {
+      constexpr int kAtOnce = 4;
+      float x[kAtOnce][E], fx[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int src = left ? __ffs(left) - 1 : 0;
+        const float* r = reinterpret_cast<const float*>(
+            __shfl_sync(kFull, reinterpret_cast<unsigned long long>(piece), src));
+        fx[k] = __shfl_sync(kFull, f, src);
+        const bool has = left != 0;
+        left &= left - 1;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = has ? __ldcg(reinterpret_cast<const float2*>(r + lane * E + e))
+                               : make_float2(0.0f, 0.0f);
+          x[k][e] = v.x;
+          x[k][e + 1] = v.y;
+        }
+        if (!has) fx[k] = 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(x[k][e], fx[k], o[e]);
+    }
+  };
   if (!own.bad && un.n > 0) {  // the pieces of the group's prefix
     const int t = (b - un.tok0) / (2 * tpt), i = (b - un.tok0) - t * 2 * tpt;
     const int r = i / tpt * kTile + i % tpt * p.G + g_row;  // the row within the item
@@ -1111,31 +1161,43 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int wt = item_weight(un, tpt, t);
     const int tiles = (item_keys(un, tpt, t) + kKeys - 1) / kKeys;
     const int n = share_count(total, split, kMinShare);
-    for (int c = share_of(total, n, pos); c < n; ++c) {
-      const int64_t x0 = share_begin(total, n, c), x1 = share_begin(total, n, c + 1);
-      if (x0 >= pos + cost) break;
-      const int j0 = cut_tile(x0 - pos, cost, wt, tiles), j1 = cut_tile(x1 - pos, cost, wt, tiles);
-      if (j0 < j1)
-        a.add(j0 == 0 ? w.first + orow * kRowF<D>
-                      : w.part + ((int64_t)c * 2 * kTile + r) * kRowF<D>,
-              lane);
+    for (int c0 = share_of(total, n, pos);
+         c0 < n && share_begin(total, n, c0) < pos + cost; c0 += 32) {
+      const int c = c0 + lane;
+      const float* piece = nullptr;
+      if (c < n) {
+        const int64_t x0 = share_begin(total, n, c) - pos, x1 = share_begin(total, n, c + 1) - pos;
+        const int j0 = cut_tile(x0, cost, wt, tiles), j1 = cut_tile(x1, cost, wt, tiles);
+        if (x0 < cost && j0 < j1)
+          piece = j0 == 0 ? w.first + orow * kRowF<D>
+                          : w.part + ((int64_t)c * 2 * kTile + r) * kRowF<D>;
+      }
+      join(piece);
     }
   }
   if (!own.bad && own.kv_len > 0) {  // and those of its own pages
     const int n_pages = own_pages(own);
-    const int64_t cost = own_cost(own), pos = w.line[p.n_groups + b] + h * cost;
+    const int64_t cost = own_cost(own), pos = own_line + h * cost;
     const int n = share_count(pages, (ctas - split) * kWarps, kMinPages);
-    for (int c = share_of(pages, n, pos); c < n; ++c) {
-      const int64_t x0 = share_begin(pages, n, c), x1 = share_begin(pages, n, c + 1);
-      if (x0 >= pos + cost) break;
-      const int i0 = own_cut(x0 - pos, n_pages), i1 = own_cut(x1 - pos, n_pages);
-      if (i0 < i1)
-        a.add(i0 == 0 ? w.first + ((int64_t)p.B * Hq + orow) * kRowF<D>
-                      : w.own + ((int64_t)c * 8 + g_row) * kRowF<D>,
-              lane);
+    for (int c0 = share_of(pages, n, pos);
+         c0 < n && share_begin(pages, n, c0) < pos + cost; c0 += 32) {
+      const int c = c0 + lane;
+      const float* piece = nullptr;
+      if (c < n) {
+        const int64_t x0 = share_begin(pages, n, c) - pos, x1 = share_begin(pages, n, c + 1) - pos;
+        const int i0 = own_cut(x0, n_pages), i1 = own_cut(x1, n_pages);
+        if (x0 < cost && i0 < i1)
+          piece = i0 == 0 ? w.first + ((int64_t)p.B * Hq + orow) * kRowF<D>
+                          : w.own + ((int64_t)c * 8 + g_row) * kRowF<D>;
+      }
+      join(piece);
     }
   }
-  a.write(p.out, p.lse, orow, lane);
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * (E / 2);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) dst[e] = pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  if (p.lse && lane == 0) p.lse[orow] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
 }
 
 // ---- host -----------------------------------------------------------------------------------
@@ -1217,12 +1279,11 @@ cudaError_t launch(const AttendParams& p, const Work& w, int ctas, cudaStream_t 
   if (e != cudaSuccess) return e;
   if (SHARED) {
     const int64_t rows = (int64_t)p.B * p.Hkv * p.G;
-    join_rows_kernel<D><<<(unsigned)((rows + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, s>>>(
-        p, w, ctas);
-  } else {
-    join_items_kernel<D><<<dim3(ctas, 2 * kTile / kJoinRows), kJoinThreads, 0, s>>>(p, w);
+    return launch_after(join_rows_kernel<D>, dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows)),
+                        kJoinThreads, s, p, w, ctas);
   }
-  return cudaGetLastError();
+  return launch_after(join_items_kernel<D>, dim3(ctas, 2 * kTile / kJoinRows), kJoinThreads, s, p,
+                      w);
 }
 
 }  // namespace

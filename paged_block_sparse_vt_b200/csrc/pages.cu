@@ -93,51 +93,58 @@ __device__ __forceinline__ Share my_share(int64_t P, int rank) {
 // The list side of a fork or growth, by CTA 0: which entries count, how many pages each needs
 // (base: exclusive sums of the needs), and the total.  A target row carries -(n - i) while the
 // call runs: the minimum over the entries that name it is its first entry.
+//
+// Lists of up to kListSmem entries stay in shared memory (and reach the other CTAs from there):
+// the search of a free page's entry takes a step per bit of n, and in global memory each was a
+// trip to L2 (a fork of 256: 28 us).
+struct Lists {
+  int *len, *need, *base;
+};
+constexpr int kListSmem = 2048;
+
 template <bool FORK>
-__device__ int read_list(const PageListParams& p, int* s_warp) {
+__device__ int read_list(const PageListParams& p, const Lists& a, int* s_warp) {
   const int n = p.n;
   for (int i = threadIdx.x; i < n; i += kScanThreads) {
-    const int row = p.targets[i];
+    const int row = p.targets[i], source = p.sources[i];
     int len = -1, need = 0, bad = 0;
     if (row < 0 || row >= p.rows) {
       bad = VT_DEV_BAD_REQ;
     } else if (FORK) {
-      const int par = p.sources[i];
-      if (par < 0 || par >= p.rows || p.seq_lens[row] != 0) {
+      if (source < 0 || source >= p.rows || p.seq_lens[row] != 0) {
         bad = VT_DEV_BAD_REQ;
       } else {
-        len = p.seq_lens[par];
+        len = p.seq_lens[source];
         if (len <= 0) bad = VT_DEV_BAD_REQ;
         else if (pages_of(len) > p.pt_stride) bad = VT_DEV_BAD_LEN;
         need = len % kPage != 0;
       }
     } else {
       len = p.seq_lens[row];
-      const int64_t grown = (int64_t)len + p.sources[i];
-      if (len < 0 || p.sources[i] < 0 || grown > p.pt_stride * kPage || grown > INT32_MAX)
+      const int64_t grown = (int64_t)len + source;
+      if (len < 0 || source < 0 || grown > p.pt_stride * kPage || grown > INT32_MAX)
         bad = VT_DEV_BAD_LEN;
       else
         need = pages_of((int)grown) - pages_of(len);
     }
     if (bad) flag(p.status, bad);
-    p.len[i] = bad ? -1 : len;
-    p.need[i] = need;
+    a.len[i] = bad ? -1 : len;
+    a.need[i] = need;
   }
   __syncthreads();
-  __threadfence();
   for (int i = threadIdx.x; i < n; i += kScanThreads)
-    if (p.len[i] >= 0) atomicMin(&p.seq_lens[p.targets[i]], i - n);
+    if (a.len[i] >= 0) atomicMin(&p.seq_lens[p.targets[i]], i - n);
   __threadfence();
   __syncthreads();
   int carry = 0;
   for (int i0 = 0; i0 < n; i0 += kScanThreads) {
     const int i = i0 + threadIdx.x;
     int need = 0;
-    if (i < n && p.len[i] >= 0) {
-      if (atomicAdd(&p.seq_lens[p.targets[i]], 0) == i - n) {
-        need = p.need[i];
+    if (i < n && a.len[i] >= 0) {
+      if (__ldcg(&p.seq_lens[p.targets[i]]) == i - n) {
+        need = a.need[i];
       } else {  // an earlier entry has the row
-        p.len[i] = -1;
+        a.len[i] = -1;
         flag(p.status, VT_DEV_BAD_REQ);
       }
     }
@@ -145,8 +152,8 @@ __device__ int read_list(const PageListParams& p, int* s_warp) {
     const int base = block_excl(need, s_warp, total);
     // sums saturate: one past 2^31 is above every pool's free pages
     if (i < n) {
-      p.need[i] = need;
-      p.base[i] = (int)min((int64_t)INT32_MAX, (int64_t)carry + base);
+      a.need[i] = need;
+      a.base[i] = (int)min((int64_t)INT32_MAX, (int64_t)carry + base);
     }
     carry = (int)min((int64_t)INT32_MAX, (int64_t)carry + total);
   }
@@ -158,13 +165,16 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
     page_list_kernel(const PageListParams p) {
   __shared__ int s_warp[kScanThreads / 32];
   __shared__ int s_free, s_need;
+  __shared__ int s_list[3][kListSmem];
   cg::cluster_group cluster = cg::this_cluster();
+  let_next_launch();
   const int rank = (int)cluster.block_rank();
   const Share sh = my_share(p.num_pages, rank);
+  const bool small = p.n <= kListSmem;
+  const Lists a = small ? Lists{s_list[0], s_list[1], s_list[2]} : Lists{p.len, p.need, p.base};
   if (rank == 0) {
-    const int need = read_list<FORK>(p, s_warp);
+    const int need = read_list<FORK>(p, a, s_warp);
     if (threadIdx.x == 0) s_need = need;
-    __threadfence();
   }
   const int n_used = count_used(p.refs, sh.lo, sh.hi, s_warp);
   if (threadIdx.x == 0) s_free = (int)(sh.hi - sh.lo) - n_used;
@@ -176,8 +186,14 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
     n_free += c;
   }
   const int total = *cluster.map_shared_rank(&s_need, 0);
-  __threadfence();
   const int want = min(total, n_free);
+  if (small && rank != 0 && before < want) {
+    const int* from = cluster.map_shared_rank(&s_list[0][0], 0);
+    for (int k = 0; k < 3; ++k)
+      for (int i = threadIdx.x; i < p.n; i += kScanThreads)
+        s_list[k][i] = from[k * kListSmem + i];
+    __syncthreads();
+  }
   // hand the free pages of this share out, lowest first
   int at = before;
   for (int64_t x0 = sh.lo; x0 < sh.hi && at < want; x0 += kScanTile) {
@@ -193,11 +209,11 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
         int lo = 0, hi = p.n - 1;  // the last entry whose base is <= k needs this page
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (__ldcg(&p.base[mid]) <= k) lo = mid; else hi = mid - 1;
+          if (a.base[mid] <= k) lo = mid; else hi = mid - 1;
         }
-        const int need = __ldcg(&p.need[lo]), base = __ldcg(&p.base[lo]);
+        const int need = a.need[lo], base = a.base[lo];
         if ((int64_t)base + need <= n_free) {
-          const int len = __ldcg(&p.len[lo]);
+          const int len = a.len[lo];
           const int page = (int)(x + e);
           // a fork's own page stands for the parent's partly filled last one
           const int slot = FORK ? len / kPage : pages_of(len) + (k - base);
@@ -211,12 +227,14 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
   }
   if (rank == 0) {
     for (int i = threadIdx.x; i < p.n; i += kScanThreads) {
-      const int len = p.len[i];
-      if (len < 0) continue;
-      const bool served = (int64_t)p.base[i] + p.need[i] <= n_free || p.need[i] == 0;
-      if (!served) flag(p.status, VT_DEV_NO_PAGE);
-      p.seq_lens[p.targets[i]] = FORK ? (served ? len : 0) : (served ? len + p.sources[i] : len);
-      if (!served) p.len[i] = -1;
+      const int len = a.len[i];
+      bool served = false;
+      if (len >= 0) {
+        served = (int64_t)a.base[i] + a.need[i] <= n_free || a.need[i] == 0;
+        if (!served) flag(p.status, VT_DEV_NO_PAGE);
+        p.seq_lens[p.targets[i]] = FORK ? (served ? len : 0) : (served ? len + p.sources[i] : len);
+      }
+      if (FORK) p.len[i] = served ? len : -1;  // for the copies
     }
   }
   cluster.sync();  // (no CTA leaves while another reads its shared memory)
@@ -279,6 +297,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 __global__ void __launch_bounds__(kCopyThreads)
     fork_apply_kernel(const PagePools pools, const PageListParams p) {
   const int i = blockIdx.x;
+  wait_for_previous();
   const int len = p.len[i];
   if (len < 0) return;
   const int32_t* from = p.page_table + (int64_t)p.sources[i] * p.pt_stride;
@@ -337,6 +356,7 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
   __shared__ int s_warp[kScanThreads / 32];
   __shared__ int s_used, s_below;
   cg::cluster_group cluster = cg::this_cluster();
+  let_next_launch();
   const int rank = (int)cluster.block_rank();
   const Share sh = my_share(p.num_pages, rank);
   const int mine = count_used(p.refs, sh.lo, sh.hi, s_warp);
@@ -386,6 +406,7 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
 
 __global__ void __launch_bounds__(kCopyThreads)
     compact_apply_kernel(const PagePools pools, const CompactParams p, int sides) {
+  wait_for_previous();
   const int moves = *p.n_moves, u = *p.n_used;
   for (int64_t w = blockIdx.x; w < (int64_t)moves * sides; w += gridDim.x) {
     const int m = (int)(w / sides), side = (int)(w - (int64_t)m * sides);
@@ -431,8 +452,7 @@ cudaError_t launch_fork(const PagePools& pools, const PageListParams& p, int sid
   page_list_kernel<true><<<kScanCtas, kScanThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fork_apply_kernel<<<dim3(p.n, sides), kCopyThreads, 0, s>>>(pools, p);
-  return cudaGetLastError();
+  return launch_after(fork_apply_kernel, dim3(p.n, sides), kCopyThreads, s, pools, p);
 }
 
 cudaError_t launch_extend(const PageListParams& p, cudaStream_t s) {
@@ -452,8 +472,7 @@ cudaError_t launch_compact(const PagePools& pools, const CompactParams& p, int s
   compact_plan_kernel<<<kScanCtas, kScanThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  compact_apply_kernel<<<sm_count * 8, kCopyThreads, 0, s>>>(pools, p, sides);
-  return cudaGetLastError();
+  return launch_after(compact_apply_kernel, dim3(sm_count * 8), kCopyThreads, s, pools, p, sides);
 }
 
 }  // namespace vt

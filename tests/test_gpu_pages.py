@@ -163,6 +163,19 @@ def test_a_page_above_the_cut_without_a_reference_stays():
     assert c.bits() == vt.VT_DEV_BAD_REF
 
 
+@pytest.mark.parametrize("n", [1500, 2048, 2049, 5000])
+def test_long_lists(n):
+    """Lists longer than a block, and than what a block keeps to itself; rows repeat in them."""
+    g = torch.Generator().manual_seed(n)
+    lens = [int(x) for x in torch.randint(0, 30, (n,), generator=g)]
+    c = Cache(lens + [0] * n, 4, int(sum(pages_of(x) for x in lens) * 1.6) + 900, hkv=1)
+    rows = [int(x) for x in torch.randint(0, n, (n,), generator=g)]
+    c.extend(rows, [int(x) for x in torch.randint(0, 20, (n,), generator=g)])
+    c.fork([int(x) for x in torch.randint(0, n, (n,), generator=g)], list(range(n, 2 * n)))
+    c.free([int(x) for x in torch.randint(0, 2 * n, (n,), generator=g)])
+    c.compact()
+
+
 def test_copy_pages():
     for kw in (dict(), dict(layout="hpd"), dict(mla=True, hkv=1, d=576)):
         c = Cache([16], 1, 40, **kw)
