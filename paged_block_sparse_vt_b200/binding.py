@@ -436,6 +436,7 @@ def vt_plan_requests(seq_lens: torch.Tensor, order: Optional[torch.Tensor] = Non
 # test per tensor, and the words for a failure only when there is one.
 
 _current_device = torch._C._cuda_getDevice
+_devices = [torch.device("cuda", i) for i in range(64)]
 
 
 def _fail(t, name: str, dtype, dev: int, contiguous: bool = True):
@@ -461,19 +462,30 @@ def _table(page_table: torch.Tensor, dev: int):
     if not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32 \
             or page_table.get_device() != dev:
         _fail(page_table, "page_table", torch.int32, dev, contiguous=False)
-    if page_table.dim() != 2 or page_table.stride(1) != 1:
+    st = page_table.stride()
+    if len(st) != 2 or st[1] != 1:
         raise VtError(VT_ERR_INVALID_ARG, "page_table", "must be [B, max_pages] with unit inner stride")
     rows, width = page_table.shape
-    return rows, page_table.stride(0) if rows > 1 else width
+    return rows, st[0] if rows > 1 else width
 
 
 def _pools(k_pool, v_pool, dev: int) -> PagedKV:
-    kv = paged_kv(k_pool, v_pool)
-    if k_pool.get_device() != dev or v_pool.get_device() != dev:
-        _fail(k_pool, "k_pool", torch.bfloat16, dev, contiguous=False)
-    if v_pool.shape[:3] != k_pool.shape[:3]:
+    """paged_kv() of pools on device ``dev`` with the same pages and heads."""
+    bf16 = torch.bfloat16
+    if not (isinstance(k_pool, torch.Tensor) and isinstance(v_pool, torch.Tensor)) \
+            or k_pool.dtype is not bf16 or v_pool.dtype is not bf16 \
+            or k_pool.get_device() != dev or v_pool.get_device() != dev:
+        paged_kv(k_pool, v_pool)
+        raise VtError(VT_ERR_INVALID_ARG, "pools", f"not on device {dev}")
+    ks, vs = k_pool.stride(), v_pool.stride()
+    if len(ks) != 4 or len(vs) != 4 or ks[3] != 1 or vs[3] != 1:
+        paged_kv(k_pool, v_pool)
+    P, ps, hkv, d = k_pool.shape
+    vp, vps, vh, dv = v_pool.shape
+    if vp != P or vps != ps or vh != hkv:
         raise VtError(VT_ERR_INVALID_ARG, "pools", "K and V pools of different shapes")
-    return kv
+    return PagedKV(k_pool.data_ptr(), v_pool.data_ptr(), P, ps, hkv, d, dv, ks[0], ks[1], ks[2],
+                   vs[0], vs[1], vs[2])
 
 
 def _status(status, dev: int):
@@ -515,7 +527,7 @@ def _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, st
 def _attend_outputs(q, out, lse, want_lse):
     dev, shape = q.get_device(), q.shape
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _vec(out, "out", torch.bfloat16, dev)
         _sized(out, "out", shape)
@@ -523,15 +535,18 @@ def _attend_outputs(q, out, lse, want_lse):
         _vec(lse, "lse", torch.float32, dev)
         _sized(lse, "lse", shape[:2])
     elif want_lse:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+        lse = torch.empty_strided((shape[0], shape[1]), (shape[1], 1), dtype=torch.float32,
+                                  device=q.device)
     return out, lse
 
 
 def _workspace(workspace, need: int, dev: int):
     """(tensor, address, bytes) of the given workspace, or of a new one (any contents)."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}") if need else None
-        return workspace, _ptr(workspace), need
+        if not need:
+            return None, None, 0
+        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=_devices[dev])
+        return workspace, workspace.data_ptr(), need
     return workspace, _vec(workspace, "workspace", torch.uint8, dev), workspace.numel()
 
 
@@ -752,7 +767,7 @@ def vt_compact_pages(k_pool, v_pool, page_table, seq_lens, refs, centroids=None,
     kv, cent = _pool_books(k_pool, v_pool, refs, centroids, dev)
     books = _books(page_table, seq_lens, refs, status, dev)
     if n_used is None:
-        n_used = torch.empty(1, dtype=torch.int32, device=refs.device)
+        n_used = torch.empty_strided((1,), (1,), dtype=torch.int32, device=refs.device)
     workspace, ws, ws_bytes = _page_ws(lib, workspace, kv.num_pages, 0, dev)
     _device_call(lib.vt_compact_pages, "vt_compact_pages", dev, kv, books, cent,
                  _vec(n_used, "n_used", torch.int32, dev), ws, ws_bytes)
