@@ -313,6 +313,7 @@ vt_status attend_common(const vt_paged_kv* kv, int batch, int Hq, const void* q,
   }
   if (batch < 0) return fail(VT_ERR_INVALID_ARG, "batch < 0");
   if (batch > 65536) return fail(VT_ERR_UNSUPPORTED, "batch > 65536");
+  if (Hq > 32767) return fail(VT_ERR_UNSUPPORTED, "num_q_heads > 32767");
   if (pt_stride < 1 || pt_stride > VT_MAX_PAGES_PER_REQUEST)
     return fail(VT_ERR_UNSUPPORTED, "pt_stride %lld outside [1, %d]", (long long)pt_stride,
                 VT_MAX_PAGES_PER_REQUEST);

@@ -87,8 +87,8 @@ struct Work {          // the workspace
   float* first;        // shared prefixes: [2][B Hq][D + 4], the rows of items' first pieces:
                        //   prefixes, then own pages
   float* own;          // shared prefixes: [ctas kWarps][8][D + 4]: rows that a warp's share continues
-  int64_t* line;       // shared prefixes: [units + 2] where each unit begins in its line, and the
-                       //   lengths of the two lines
+  int64_t* line;       // shared prefixes: [units] where each unit begins in its line
+  Line* lines;         // shared prefixes: the two lines; lines[0].total -1: nothing was done
 };
 
 // A partial row: O, then m (scaled, base 2) and l; padded to 16 bytes.
@@ -454,25 +454,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     umma::mbar_fence_init();
   }
+  // (costs are worked out before it is known that the starts are in order: no index depends on
+  // them but `row` and `tok0`, which are not used here)
+  const int per = (units + kPlan - 1) / kPlan, entries = (units + per - 1) / per;
+  uint32_t bad_len = 0;
+  for (int e = threadIdx.x; e < entries; e += kThreads) {
+    int64_t c[2] = {0, 0};
+    for (int u = e * per; u < min(units, (e + 1) * per); ++u) {
+      const Unit x = load_unit<SHARED>(p, u);
+      bad_len |= x.bad;
+      if (SHARED && u >= p.n_groups) c[1] += p.Hkv * own_cost(x);
+      else c[0] += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
+    }
+    table0[e + 1] = c[0];
+    if (SHARED) table1[e + 1] = c[1];
+  }
   umma::fence_before_sync();
   fine = __syncthreads_and(fine);
   umma::fence_after_sync();
   const uint32_t tm = sh.tmem;
-
-  const int per = (units + kPlan - 1) / kPlan, entries = (units + per - 1) / per;
-  if (fine)
-    for (int e = threadIdx.x; e < entries; e += kThreads) {
-      int64_t c[2] = {0, 0};
-      for (int u = e * per; u < min(units, (e + 1) * per); ++u) {
-        const Unit x = load_unit<SHARED>(p, u);
-        if (x.bad && cta == 0) flag(p.status, VT_DEV_BAD_LEN);
-        if (SHARED && u >= p.n_groups) c[1] += p.Hkv * own_cost(x);
-        else c[0] += p.Hkv * cost_before(x, tpt, unit_items(x, tpt));
-      }
-      table0[e + 1] = c[0];
-      if (SHARED) table1[e + 1] = c[1];
-    }
-  __syncthreads();
+  if (fine && bad_len && cta == 0) flag(p.status, VT_DEV_BAD_LEN);
   if (fine && warp < (SHARED ? 2 : 1)) {
     int64_t* line = warp ? table1 : table0;
     const int run = (entries + 31) / 32;
@@ -496,9 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!fine && cta == 0 && threadIdx.x == 0) flag(p.status, VT_DEV_BAD_START);
   const int64_t total = fine ? table0[entries] : 0, pages = SHARED && fine ? table1[entries] : 0;
   const int split = SHARED ? first_own(total, pages, gridDim.x) : gridDim.x;
-  const int n_cta = share_count(total, max(split, 1), kMinShare);
+  const Line tiles_line = make_line(total, max(split, 1), kMinShare);
 
-  if (SHARED && cta == 0) {  // where the units begin, for the joining kernel; -1: nothing was done
+  // What the joining kernel needs to find the pieces: from a CTA without work, if there is one.
+  if (SHARED && cta == (tiles_line.n < split ? tiles_line.n : (int)gridDim.x - 1)) {
     if (fine) {
       for (int e = threadIdx.x; e < entries; e += kThreads) {
         int64_t c[2] = {table0[e], table1[e]};
@@ -511,18 +513,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (threadIdx.x == 0) {
-      w.line[units] = fine ? total : -1;
-      w.line[units + 1] = pages;
+      w.lines[0] = tiles_line;
+      if (!fine) w.lines[0].total = -1;
+      w.lines[1] = make_line(pages, max(((int)gridDim.x - split) * kWarps, 1), kMinPages);
     }
-    __syncthreads();  // (before q overwrites the tables)
+    __syncthreads();  // (before what comes into shared memory overwrites the tables)
   }
 
   if (SHARED && cta >= split) {
     // ---- own pages: a warp, a share ------------------------------------------------------------
-    const int n_warp = share_count(pages, (gridDim.x - split) * kWarps, kMinPages);
+    const Line own_line = make_line(pages, (gridDim.x - split) * kWarps, kMinPages);
     const int ws = (cta - split) * kWarps + warp;
-    const int64_t x0 = ws < n_warp ? share_begin(pages, n_warp, ws) : 0;
-    const int64_t x1 = ws < n_warp ? share_begin(pages, n_warp, ws + 1) : 0;
+    const int64_t x0 = ws < own_line.n ? share_begin(own_line, ws) : 0;
+    const int64_t x1 = ws < own_line.n ? share_begin(own_line, ws + 1) : 0;
     OwnCursor cur;
     if (x0 < x1) cur.seek(p, table1, entries, per, x0);
     __syncthreads();  // (before the pages overwrite the tables)
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   const int64_t* line = table0;
-  const bool work = total > 0 && cta < n_cta;
+  const bool work = total > 0 && cta < tiles_line.n;
   if (warp >= kLoadWarp) {
   regs_less<kRegsOther>();
   if (warp == kLoadWarp) {
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t filled = 0;  // stage uses, for the drain behind an abort
     bool go = true;
     if (work) {
-      const int64_t x0 = share_begin(total, n_cta, cta), x1 = share_begin(total, n_cta, cta + 1);
+      const int64_t x0 = share_begin(tiles_line, cta), x1 = share_begin(tiles_line, cta + 1);
       int lo = 0, hi = entries - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -1090,23 +1093,21 @@ __global__ void __launch_bounds__(kJoinThreads)
 // are read at once: one after the other, a prefix of 18 pieces took 18 trips to memory (23 us).
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
-    join_rows_kernel(const AttendParams p, const Work w, int ctas) {
+    join_rows_kernel(const AttendParams p, const Work w) {
   constexpr int E = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hq = p.Hkv * p.G, tpt = kTile / p.G;
-  const int64_t orow = (int64_t)blockIdx.x * kJoinRows + warp;
-  if (orow >= (int64_t)p.B * Hq) return;
-  const int b = (int)(orow / Hq), hq = (int)(orow - (int64_t)b * Hq);
+  const int orow = blockIdx.x * kJoinRows + warp;  // (B Hq < 2^31, as api.cu checks)
+  if (orow >= p.B * Hq) return;
+  const int b = orow / Hq, hq = orow - b * Hq;
   const int h = hq / p.G, g_row = hq - h * p.G;
-  const int units = p.n_groups + p.B;
   wait_for_previous();
-  const int64_t total = w.line[units], pages = w.line[units + 1];
-  const int64_t own_line = w.line[p.n_groups + b];
-  if (total < 0) return;
+  const Line tl = w.lines[0], ol = w.lines[1];
+  const int64_t own_at = w.line[p.n_groups + b];
+  if (tl.total < 0) return;
   const int g = group_of(p, b);
   if (g < 0) return;
   const Unit own = load_unit<true>(p, p.n_groups + b), un = load_unit<true>(p, g);
-  const int split = first_own(total, pages, ctas);
   float o[E], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
@@ -1160,16 +1161,14 @@ __global__ void __launch_bounds__(kJoinThreads)
                         cost_before(un, tpt, t);
     const int wt = item_weight(un, tpt, t);
     const int tiles = (item_keys(un, tpt, t) + kKeys - 1) / kKeys;
-    const int n = share_count(total, split, kMinShare);
-    for (int c0 = share_of(total, n, pos);
-         c0 < n && share_begin(total, n, c0) < pos + cost; c0 += 32) {
+    for (int c0 = share_of(tl, pos); c0 < tl.n && share_begin(tl, c0) < pos + cost; c0 += 32) {
       const int c = c0 + lane;
       const float* piece = nullptr;
-      if (c < n) {
-        const int64_t x0 = share_begin(total, n, c) - pos, x1 = share_begin(total, n, c + 1) - pos;
+      if (c < tl.n) {
+        const int64_t x0 = share_begin(tl, c) - pos, x1 = share_begin(tl, c + 1) - pos;
         const int j0 = cut_tile(x0, cost, wt, tiles), j1 = cut_tile(x1, cost, wt, tiles);
         if (x0 < cost && j0 < j1)
-          piece = j0 == 0 ? w.first + orow * kRowF<D>
+          piece = j0 == 0 ? w.first + (int64_t)orow * kRowF<D>
                           : w.part + ((int64_t)c * 2 * kTile + r) * kRowF<D>;
       }
       join(piece);
@@ -1177,14 +1176,12 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
   if (!own.bad && own.kv_len > 0) {  // and those of its own pages
     const int n_pages = own_pages(own);
-    const int64_t cost = own_cost(own), pos = own_line + h * cost;
-    const int n = share_count(pages, (ctas - split) * kWarps, kMinPages);
-    for (int c0 = share_of(pages, n, pos);
-         c0 < n && share_begin(pages, n, c0) < pos + cost; c0 += 32) {
+    const int64_t cost = own_cost(own), pos = own_at + h * cost;
+    for (int c0 = share_of(ol, pos); c0 < ol.n && share_begin(ol, c0) < pos + cost; c0 += 32) {
       const int c = c0 + lane;
       const float* piece = nullptr;
-      if (c < n) {
-        const int64_t x0 = share_begin(pages, n, c) - pos, x1 = share_begin(pages, n, c + 1) - pos;
+      if (c < ol.n) {
+        const int64_t x0 = share_begin(ol, c) - pos, x1 = share_begin(ol, c + 1) - pos;
         const int i0 = own_cut(x0, n_pages), i1 = own_cut(x1, n_pages);
         if (x0 < cost && i0 < i1)
           piece = i0 == 0 ? w.first + ((int64_t)p.B * Hq + orow) * kRowF<D>
@@ -1194,7 +1191,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * (E / 2);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (int64_t)orow * D) + lane * (E / 2);
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) dst[e] = pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
   if (p.lse && lane == 0) p.lse[orow] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
@@ -1219,7 +1216,8 @@ size_t lay_out(const AttendParams& p, int ctas, void* ws, Work* w) {
   x.part = reinterpret_cast<float*>(take((size_t)(shared ? 1 : 2) * ctas * 2 * kTile * row));
   x.first = reinterpret_cast<float*>(take(shared ? 2 * (size_t)p.B * p.Hkv * p.G * row : 0));
   x.own = reinterpret_cast<float*>(take(shared ? (size_t)ctas * kWarps * 8 * row : 0));
-  x.line = reinterpret_cast<int64_t*>(take(shared ? ((size_t)p.n_groups + p.B + 2) * 8 : 0));
+  x.line = reinterpret_cast<int64_t*>(take(shared ? ((size_t)p.n_groups + p.B) * 8 : 0));
+  x.lines = reinterpret_cast<Line*>(take(shared ? 2 * sizeof(Line) : 0));
   if (w) *w = x;
   return at;
 }
@@ -1280,7 +1278,7 @@ cudaError_t launch(const AttendParams& p, const Work& w, int ctas, cudaStream_t 
   if (SHARED) {
     const int64_t rows = (int64_t)p.B * p.Hkv * p.G;
     return launch_after(join_rows_kernel<D>, dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows)),
-                        kJoinThreads, s, p, w, ctas);
+                        kJoinThreads, s, p, w);
   }
   return launch_after(join_items_kernel<D>, dim3(ctas, 2 * kTile / kJoinRows), kJoinThreads, s, p,
                       w);

@@ -35,7 +35,7 @@ constexpr int kMinPages = 4;      // no warp takes less
 // A page of one head in the costs of the first line, measured: 256 requests on one prefix of 65536
 // tokens took 791 us with 20, 639 with 35, 565 with 50, 552 with 70; 128 requests with long own
 // parts 176, 184, 185, 215.
-constexpr int kOwnPage = 50;
+constexpr int kOwnPage = 45;
 
 struct Unit {
   int tok0, n;     // its query tokens (0: no items)
@@ -99,21 +99,36 @@ VT_HD int first_own(int64_t tiles, int64_t pages, int ctas) {
   return ctas - (n < 1 ? 1 : n > ctas - 1 ? ctas - 1 : n);
 }
 
-// Those (of `most`) that share a line of length `total`, no share less than `least`, and where
-// the c-th share begins.
+// Those (of `most`) that share a line of length `total`, no share less than `least`.
 VT_HD int share_count(int64_t total, int most, int64_t least) {
   const int64_t n = total / least;
   return n < 1 ? 1 : n < most ? (int)n : most;
 }
-VT_HD int64_t share_begin(int64_t total, int n, int c) {
-  return total / n * c + total % n * c / n;
+// A line and its n equal shares; the c-th begins at floor(total c / n).
+struct Line {
+  int64_t total, base;  // base = total / n
+  double inv;           // n / total
+  int n, rem;           // rem = total % n
+};
+VT_HD Line make_line(int64_t total, int most, int64_t least) {
+  Line x;
+  x.total = total;
+  x.n = share_count(total, most, least);
+  x.base = total / x.n;
+  x.rem = (int)(total - x.base * x.n);
+  x.inv = total > 0 ? (double)x.n / (double)total : 0.0;
+  return x;
+}
+// (rem c < n^2, and n is at most 12 per SM: far inside 32 bits)
+VT_HD int64_t share_begin(const Line& x, int c) {
+  return x.base * c + (unsigned)x.rem * (unsigned)c / (unsigned)x.n;
 }
 // The share that position x < total is in.
-VT_HD int share_of(int64_t total, int n, int64_t x) {
-  int c = (int)((double)x / (double)total * n);
-  c = c < 0 ? 0 : c >= n ? n - 1 : c;
-  while (c > 0 && share_begin(total, n, c) > x) --c;
-  while (c + 1 < n && share_begin(total, n, c + 1) <= x) ++c;
+VT_HD int share_of(const Line& x, int64_t pos) {
+  int c = (int)((double)pos * x.inv);
+  c = c < 0 ? 0 : c >= x.n ? x.n - 1 : c;
+  while (c > 0 && share_begin(x, c) > pos) --c;
+  while (c + 1 < x.n && share_begin(x, c + 1) <= pos) ++c;
   return c;
 }
 

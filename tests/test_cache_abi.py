@@ -47,6 +47,7 @@ _COMMON = [
     (dict(sk_p=1 << 39), {}, UNS),
     ({}, dict(num_q_heads=30), INV),
     ({}, dict(num_q_heads=72), UNS),
+    (dict(num_kv_heads=32768, sk_h=128, sv_h=128), dict(num_q_heads=32768, sq_t=1 << 23), UNS),
     ({}, dict(batch=-1), INV),
     ({}, dict(batch=65537), UNS),
     ({}, dict(batch=0), OK),
@@ -78,6 +79,7 @@ def _shared(lib, kv, over, out=FAKE + 0x600000, ws=FAKE + 0x8000000, ws_bytes=BI
              prefix_pages=FAKE + 0x305000, page_table=FAKE + 0x310000, pt_stride=64,
              seq_lens=FAKE + 0x400000, sm_scale=0.088, status=None)
     f.update(over)
+    f.pop("sq_t", None)
     a = binding.SharedPrefixArgs(**f)
     need = lib.vt_shared_prefix_workspace_size(ctypes.byref(kv), ctypes.byref(a))
     return lib.vt_shared_prefix_decode(ctypes.byref(kv), ctypes.byref(a), out, None, ws, ws_bytes,
