@@ -244,6 +244,7 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
 // each thread.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
+constexpr int kApplyCtas = 8;  // per SM; a CTA takes several moves
 
 __device__ __forceinline__ void copy_page(const PoolView& v, int64_t dst, int64_t src) {
   const int per_head = v.dim / 8, per_tok = v.heads * per_head, total = kPage * per_tok;
@@ -265,8 +266,9 @@ __device__ __forceinline__ void copy_page(const PoolView& v, int64_t dst, int64_
   }
 }
 
+// what is behind a page's first kCopyThreads pieces of centroids
 __device__ __forceinline__ void copy_centroids(float* c, int64_t row, int64_t dst, int64_t src) {
-  for (int64_t i = threadIdx.x; i < row / 4; i += kCopyThreads)
+  for (int64_t i = threadIdx.x + kCopyThreads; i < row / 4; i += kCopyThreads)
     reinterpret_cast<float4*>(c + dst * row)[i] = ld_stream_f4(c + src * row + i * 4);
 }
 
@@ -274,7 +276,14 @@ __device__ __forceinline__ void copy_centroids(float* c, int64_t row, int64_t ds
 __device__ __forceinline__ void copy_side(const PagePools& pools, int side, int64_t dst,
                                           int64_t src) {
   if (side == 0) {
+    // (the centroids' first piece is in flight beside the page)
+    const bool cent = pools.centroids && threadIdx.x < pools.cent_row / 4;
+    float4 first;
+    if (cent)
+      first = ld_stream_f4(pools.centroids + src * pools.cent_row + threadIdx.x * 4);
     copy_page(pools.k, dst, src);
+    if (cent)
+      reinterpret_cast<float4*>(pools.centroids + dst * pools.cent_row)[threadIdx.x] = first;
     if (pools.centroids) copy_centroids(pools.centroids, pools.cent_row, dst, src);
   } else {
     copy_page(pools.v, dst, src);
@@ -405,18 +414,18 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
-    compact_apply_kernel(const PagePools pools, const CompactParams p, int sides) {
+    compact_apply_kernel(const PagePools pools, const CompactParams p) {
   wait_for_previous();
   const int moves = *p.n_moves, u = *p.n_used;
-  for (int64_t w = blockIdx.x; w < (int64_t)moves * sides; w += gridDim.x) {
-    const int m = (int)(w / sides), side = (int)(w - (int64_t)m * sides);
+  for (int m = blockIdx.x; m < moves; m += gridDim.x) {
     const int s = p.src[m], d = p.dst[m];
-    copy_side(pools, side, d, s);
-    if (side == 0 && threadIdx.x == 0) {
+    copy_side(pools, blockIdx.y, d, s);
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
       p.refs[d] = p.refs[s];
       p.refs[s] = 0;
     }
   }
+  if (blockIdx.y != 0) return;
   for (int row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const int len = p.seq_lens[row];
     if (len <= 0) continue;
@@ -472,7 +481,7 @@ cudaError_t launch_compact(const PagePools& pools, const CompactParams& p, int s
   compact_plan_kernel<<<kScanCtas, kScanThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_after(compact_apply_kernel, dim3(sm_count * 8), kCopyThreads, s, pools, p, sides);
+  return launch_after(compact_apply_kernel, dim3(sm_count * kApplyCtas, sides), kCopyThreads, s, pools, p);
 }
 
 }  // namespace vt
