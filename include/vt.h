@@ -348,8 +348,8 @@ typedef struct {
 vt_status vt_prefill(const vt_paged_kv* kv, const vt_prefill_args* a, void* out, float* lse,
                      void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace vt_prefill needs for these shapes on the current device; 0 for arguments
- * that vt_prefill rejects and for an empty batch. */
+/* Bytes of workspace vt_prefill needs for these shapes on the current device; 0 (no workspace,
+ * NULL will do) for sizes of one CTA's work, an empty batch and arguments that it rejects. */
 size_t vt_prefill_workspace_size(const vt_paged_kv* kv, const vt_prefill_args* a);
 
 /*

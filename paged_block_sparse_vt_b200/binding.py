@@ -578,13 +578,15 @@ def _device_call(fn, where: str, dev: int, *args) -> None:
 
 
 def _prefill_ws(lib, dev: int, kv: PagedKV, a: PrefillArgs) -> int:
-    if a.batch == 0 or a.num_tokens == 0:
-        return 0
-    return _ws_size(("prefill", dev, kv.head_dim), lambda: _on_device(
-        dev, lib.vt_prefill_workspace_size, ctypes.byref(kv), ctypes.byref(a)))
+    if a.num_tokens < 1024:  # (small calls need none; larger ones the same, whatever their sizes)
+        return int(_on_device(dev, lib.vt_prefill_workspace_size, kv, a))
+    return _ws_size(("prefill", dev, kv.head_dim),
+                    lambda: _on_device(dev, lib.vt_prefill_workspace_size, kv, a))
 
 
 def _on_device(dev: int, fn, *args):
+    if _current_device() == dev:
+        return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args)
 
@@ -636,8 +638,7 @@ def _shared_ws(lib, dev: int, kv: PagedKV, a: SharedPrefixArgs) -> int:
     if a.batch == 0 or a.num_groups == 0:
         return 0
     return _ws_size(("shared", dev, kv.head_dim, a.batch, a.num_q_heads, a.num_groups),
-                    lambda: _on_device(dev, lib.vt_shared_prefix_workspace_size, ctypes.byref(kv),
-                                       ctypes.byref(a)))
+                    lambda: _on_device(dev, lib.vt_shared_prefix_workspace_size, kv, a))
 
 
 def shared_prefix_workspace(q, k_pool, v_pool, page_table, seq_lens, group_start,
@@ -865,6 +866,48 @@ def prepare_sparse_decode_step(q, k_pool, v_pool, page_table, seq_lens, centroid
             P(centroids.data_ptr())) + fused._args[2:]
     return PreparedCall(lib.vt_sparse_decode_step, args, q.get_device(), "vt_sparse_decode_step",
                         fused._keep + (fill_pages,), fused.result)
+
+
+def _prepare_attend(lib, where: str, dev: int, kv, a, need: int, q, out, lse, workspace, keep):
+    _vec(out, "out", torch.bfloat16, dev)
+    _sized(out, "out", q.shape)
+    if lse is not None:
+        _vec(lse, "lse", torch.float32, dev)
+        _sized(lse, "lse", q.shape[:2])
+    if need and workspace is None:
+        raise VtError(VT_ERR_INVALID_ARG, "workspace", f"{need} bytes needed (see {where})")
+    ws = None if workspace is None else _vec(workspace, "workspace", torch.uint8, dev)
+    P = ctypes.c_void_p
+    args = (ctypes.byref(kv), ctypes.byref(a), P(out.data_ptr()), P(_ptr(lse)), P(ws),
+            ctypes.c_size_t(0 if workspace is None else workspace.numel()))
+    return PreparedCall(getattr(lib, where), args, dev, where,
+                        (kv, a, q, out, lse, workspace) + keep, (out, lse))
+
+
+def prepare_prefill(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, out, lse=None,
+                    status=None, workspace=None) -> PreparedCall:
+    """vt_prefill bound to these tensors (``q_start`` and ``seq_lens`` included: their contents may
+    change between runs); ``run()`` returns (out, lse).  ``workspace``: from prefill_workspace();
+    required when the shapes need one."""
+    lib = load_library()
+    kv, a = _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, status)
+    dev = q.get_device()
+    return _prepare_attend(lib, "vt_prefill", dev, kv, a, _prefill_ws(lib, dev, kv, a), q, out, lse,
+                           workspace, (k_pool, v_pool, page_table, seq_lens, q_start, status))
+
+
+def prepare_shared_prefix_decode(q, k_pool, v_pool, page_table, seq_lens, group_start,
+                                 prefix_pages, sm_scale, out, lse=None, status=None,
+                                 workspace=None) -> PreparedCall:
+    """vt_shared_prefix_decode bound to these tensors; ``run()`` returns (out, lse).
+    ``workspace``: from shared_prefix_workspace(); required when the shapes need one."""
+    lib = load_library()
+    kv, a = _shared_args(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pages,
+                         sm_scale, status)
+    dev = q.get_device()
+    return _prepare_attend(lib, "vt_shared_prefix_decode", dev, kv, a, _shared_ws(lib, dev, kv, a),
+                           q, out, lse, workspace, (k_pool, v_pool, page_table, seq_lens,
+                                                    group_start, prefix_pages, status))
 
 
 def vt_abi_version() -> int:

@@ -386,8 +386,10 @@ vt_status run_attend(AttendParams& p, void* out, float* lse, void* ws, size_t ws
   if (!out) return fail(VT_ERR_INVALID_ARG, "out is NULL");
   if (!aligned16(out)) return fail(VT_ERR_UNSUPPORTED, "out not 16-byte aligned");
   const int sms = sm_count();
-  vt_status s = check_workspace(ws, ws_bytes, attend_workspace_bytes(p, sms));
-  if (s != VT_OK) return s;
+  if (const size_t need = attend_workspace_bytes(p, sms)) {
+    vt_status s = check_workspace(ws, ws_bytes, need);
+    if (s != VT_OK) return s;
+  }
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   cudaError_t e = launch_attend(p, ws, sms, static_cast<cudaStream_t>(stream));

@@ -28,6 +28,8 @@
 // a second launch joins those: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "attend_params.cuh"
 #include "attend_plan.cuh"
 #include "common.cuh"
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   regs_less<kRegsOther>();
   if (warp == kLoadWarp) {
     // ---- loading -----------------------------------------------------------------------------
-    if (lane == 0 && !SHARED) {
+    if (lane == 0 && !SHARED && w.head) {
       w.head[2 * cta].valid = 0;
       w.head[2 * cta + 1].valid = 0;
     }
@@ -1201,9 +1203,20 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Whether prompts of these sizes can be more than one CTA's share, whatever their lengths: if
+// not, no item is cut, and there is nothing to join and no workspace.
+bool may_split(const AttendParams& p) {
+  const int64_t tpt = kTile / p.G, items = p.Hkv * (p.T / (2 * tpt) + std::min<int64_t>(p.B, p.T));
+  return items * kCostTwo * (kCostItem + p.pt_stride * kPage) >= 2 * kMinShare;
+}
+
 // Fills w from ws (NULL: only the size is wanted) and returns the bytes.
 size_t lay_out(const AttendParams& p, int ctas, void* ws, Work* w) {
   const bool shared = p.prefix_pages != nullptr;
+  if (!shared && !may_split(p)) {
+    if (w) *w = Work{};
+    return 0;
+  }
   const size_t row = (size_t)(p.D + 4) * 4;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1280,6 +1293,7 @@ cudaError_t launch(const AttendParams& p, const Work& w, int ctas, cudaStream_t 
     return launch_after(join_rows_kernel<D>, dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows)),
                         kJoinThreads, s, p, w);
   }
+  if (!w.head) return cudaSuccess;
   return launch_after(join_items_kernel<D>, dim3(ctas, 2 * kTile / kJoinRows), kJoinThreads, s, p,
                       w);
 }

@@ -124,6 +124,9 @@ def test_attention_output_and_workspace_refusals(lib, call):
     assert call(lib, _kv(), {}, ws_bytes=need - 1)[0] == INV
     assert b"workspace" in lib.vt_last_error_detail()
     assert call(lib, _kv(), {}, ws=FAKE + 16)[0] == INV
+    # one CTA's work needs none
+    assert _prefill(lib, _kv(num_kv_heads=1), dict(num_q_heads=2, batch=1, num_tokens=7, sq_t=256,
+                                                   pt_stride=4), out=None) == (INV, 0)
     assert lib.vt_prefill(ctypes.byref(_kv()), None, FAKE, None, FAKE, BIG, None) == INV
     assert lib.vt_shared_prefix_decode(None, None, FAKE, None, FAKE, BIG, None) == INV
 

@@ -223,6 +223,30 @@ def test_graphs_that_share_a_workspace_and_new_lengths():
             check_attend(out, None, attend_ref(*c, lens, scale))
 
 
+@pytest.mark.parametrize("q_lens,ctx", [([300, 41], [90, 2000]), ([9], [0])])
+def test_prepared(q_lens, ctx):
+    """The prepared call gives what the plain one gives, also after its inputs changed in place."""
+    q, k, v, table, seq = case(q_lens, ctx, 4, 2, 128)
+    start, scale = starts(q_lens), scale_of(128)
+    ws = vt.prefill_workspace(q, k, v, table, seq, start)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    call = vt.prepare_prefill(q, k, v, table, seq, start, scale, out, lse, workspace=ws)
+    for _ in range(2):
+        assert call.run() == (out, lse)
+        want, want_lse = vt.vt_prefill(q, k, v, table, seq, start, scale)
+        n = int(start[-1])                       # (rows behind it are nobody's)
+        assert torch.equal(out[:n], want[:n]) and torch.equal(lse[:n], want_lse[:n])
+        q.mul_(0.5)
+        seq.sub_(1)
+        start.clamp_(max=int(start[-1]) - 1)
+        seq[-1:].clamp_(min=int(start[-1] - start[-2]))
+    if ws is not None:
+        with pytest.raises(vt.VtError):
+            vt.prepare_prefill(q, k, v, table, seq, start, scale, out)
+    with pytest.raises(vt.VtError):
+        vt.prepare_prefill(q, k, v, table, seq, start, scale, out[:1], workspace=ws)
+
+
 def test_two_streams_at_once():
     q_lens, ctx = [400, 100], [900, 0]
     cases = [case(q_lens, ctx, 4, 2, 64, seed=s) for s in (1, 2)]
@@ -243,13 +267,13 @@ def test_two_streams_at_once():
 
 
 def test_binding_refusals():
-    q, k, v, table, seq = case([5], [0], 2, 1, 64)
-    start = starts([5])
+    q, k, v, table, seq = case([300], [300], 2, 1, 64)   # (of a size that needs a workspace)
+    start = starts([300])
     bad = [dict(q=q.float()), dict(q=q[..., ::2]), dict(q=q.transpose(0, 1)), dict(seq_lens=seq.long()),
            dict(q_start=start[:1]), dict(k_pool=k.half()), dict(out=q.float()),
            dict(out=q[:4].clone()), dict(lse=torch.empty(5, 1, device="cuda")),
            dict(workspace=torch.empty(0, dtype=torch.uint8, device="cuda")),
-           dict(sm_scale=-1.0), dict(page_table=table.t().expand(1, 1)[:, :1].long())]
+           dict(sm_scale=-1.0), dict(page_table=table.long())]
     for over in bad:
         kw = dict(q=q, k_pool=k, v_pool=v, page_table=table, seq_lens=seq, q_start=start,
                   sm_scale=0.1)

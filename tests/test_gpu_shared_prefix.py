@@ -183,6 +183,21 @@ def test_repeats_graphs_and_a_shared_workspace():
     check_attend(*got[0], ref_of(a))
 
 
+def test_prepared():
+    c = build(*GROUPS["groups"], 8, 2, 128)
+    args = ("q", "k_pool", "v_pool", "page_table", "seq_lens", "group_start", "prefix_pages")
+    ws = vt.shared_prefix_workspace(*(c[n] for n in args))
+    out, lse = torch.empty_like(c["q"]), torch.empty(c["q"].shape[:2], device="cuda")
+    call = vt.prepare_shared_prefix_decode(**c, out=out, lse=lse, workspace=ws)
+    for _ in range(2):
+        assert call.run() == (out, lse)
+        want, want_lse = vt.vt_shared_prefix_decode(**c)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        c["q"].mul_(0.5)
+    with pytest.raises(vt.VtError):
+        vt.prepare_shared_prefix_decode(**c, out=out)
+
+
 def test_binding_refusals():
     c = build([2], [1], [3, 4], 2, 1, 64)
     for over in (dict(q=c["q"].float()), dict(q=c["q"][:1]), dict(group_start=c["group_start"][:1]),
