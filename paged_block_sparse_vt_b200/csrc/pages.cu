@@ -20,6 +20,9 @@ namespace vt {
 namespace {
 
 constexpr int kScanCtas = 8;
+// A pool of up to this many pages is scanned by one CTA: four reads each of its threads, against
+// a cluster's launch and two barriers of eight.
+constexpr int64_t kOneCta = 16384;
 constexpr int kScanThreads = 1024;
 constexpr int kScanTile = kScanThreads * 4;  // counts per step: an int4 each
 
@@ -81,9 +84,10 @@ struct Share {
   int64_t lo, hi;  // this CTA's pages
 };
 
+template <int CTAS>
 __device__ __forceinline__ Share my_share(int64_t P, int rank) {
   const int64_t tiles = (P + kScanTile - 1) / kScanTile;
-  const int64_t per = (tiles + kScanCtas - 1) / kScanCtas * kScanTile;
+  const int64_t per = (tiles + CTAS - 1) / CTAS * kScanTile;
   Share s;
   s.lo = min(P, per * rank);
   s.hi = min(P, s.lo + per);
@@ -160,8 +164,8 @@ __device__ int read_list(const PageListParams& p, const Lists& a, int* s_warp) {
   return carry;
 }
 
-template <bool FORK>
-__global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads, 1)
+template <bool FORK, int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kScanThreads, 1)
     page_list_kernel(const PageListParams p) {
   __shared__ int s_warp[kScanThreads / 32];
   __shared__ int s_free, s_need;
@@ -169,7 +173,7 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
   cg::cluster_group cluster = cg::this_cluster();
   let_next_launch();
   const int rank = (int)cluster.block_rank();
-  const Share sh = my_share(p.num_pages, rank);
+  const Share sh = my_share<CTAS>(p.num_pages, rank);
   const bool small = p.n <= kListSmem;
   const Lists a = small ? Lists{s_list[0], s_list[1], s_list[2]} : Lists{p.len, p.need, p.base};
   if (rank == 0) {
@@ -180,7 +184,7 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
   if (threadIdx.x == 0) s_free = (int)(sh.hi - sh.lo) - n_used;
   cluster.sync();
   int before = 0, n_free = 0;
-  for (int r = 0; r < kScanCtas; ++r) {
+  for (int r = 0; r < CTAS; ++r) {
     const int c = *cluster.map_shared_rank(&s_free, r);
     before += r < rank ? c : 0;
     n_free += c;
@@ -360,19 +364,20 @@ __global__ void __launch_bounds__(kCopyThreads)
 // Moves of a compaction.  With used(x) = #{y < x : refs[y] > 0} and u = used(P): the free page
 // x < u has rank x - used(x) among the free ones, the used page x >= u has rank
 // used(x) - used(u) among those that move.
-__global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads, 1)
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kScanThreads, 1)
     compact_plan_kernel(const CompactParams p) {
   __shared__ int s_warp[kScanThreads / 32];
   __shared__ int s_used, s_below;
   cg::cluster_group cluster = cg::this_cluster();
   let_next_launch();
   const int rank = (int)cluster.block_rank();
-  const Share sh = my_share(p.num_pages, rank);
+  const Share sh = my_share<CTAS>(p.num_pages, rank);
   const int mine = count_used(p.refs, sh.lo, sh.hi, s_warp);
   if (threadIdx.x == 0) s_used = mine;
   cluster.sync();
   int before = 0, u = 0;
-  for (int r = 0; r < kScanCtas; ++r) {
+  for (int r = 0; r < CTAS; ++r) {
     const int c = *cluster.map_shared_rank(&s_used, r);
     before += r < rank ? c : 0;
     u += c;
@@ -383,7 +388,7 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
   if (threadIdx.x == 0) s_below = below;
   cluster.sync();
   int used_u = 0;
-  for (int r = 0; r < kScanCtas; ++r) used_u += *cluster.map_shared_rank(&s_below, r);
+  for (int r = 0; r < CTAS; ++r) used_u += *cluster.map_shared_rank(&s_below, r);
   if (rank == 0 && threadIdx.x == 0) {
     *p.n_used = u;
     *p.n_moves = u - used_u;
@@ -458,14 +463,16 @@ cudaError_t launch_copy_pages(const PagePools& pools, const int32_t* src, const 
 
 cudaError_t launch_fork(const PagePools& pools, const PageListParams& p, int sides,
                         cudaStream_t s) {
-  page_list_kernel<true><<<kScanCtas, kScanThreads, 0, s>>>(p);
+  if (p.num_pages <= kOneCta) page_list_kernel<true, 1><<<1, kScanThreads, 0, s>>>(p);
+  else page_list_kernel<true, kScanCtas><<<kScanCtas, kScanThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_after(fork_apply_kernel, dim3(p.n, sides), kCopyThreads, s, pools, p);
 }
 
 cudaError_t launch_extend(const PageListParams& p, cudaStream_t s) {
-  page_list_kernel<false><<<kScanCtas, kScanThreads, 0, s>>>(p);
+  if (p.num_pages <= kOneCta) page_list_kernel<false, 1><<<1, kScanThreads, 0, s>>>(p);
+  else page_list_kernel<false, kScanCtas><<<kScanCtas, kScanThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -478,7 +485,8 @@ cudaError_t launch_free(const vt_page_books& b, int64_t num_pages, const int32_t
 
 cudaError_t launch_compact(const PagePools& pools, const CompactParams& p, int sides, int sm_count,
                            cudaStream_t s) {
-  compact_plan_kernel<<<kScanCtas, kScanThreads, 0, s>>>(p);
+  if (p.num_pages <= kOneCta) compact_plan_kernel<1><<<1, kScanThreads, 0, s>>>(p);
+  else compact_plan_kernel<kScanCtas><<<kScanCtas, kScanThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_after(compact_apply_kernel, dim3(sm_count * kApplyCtas, sides), kCopyThreads, s, pools, p);
