@@ -20,8 +20,8 @@
  *   - Every data pointer is DEVICE memory owned by the caller.  The library
  *     never allocates, frees or synchronises; each call enqueues its kernels
  *     on `stream` (a cudaStream_t passed as void*; NULL = legacy default
- *     stream) and returns.  Only vt_sparse_decode_fused takes a workspace
- *     (see vt_fused_workspace_size).
+ *     stream) and returns.  Calls that need scratch memory take a workspace
+ *     of the caller's, whose size a call of its own gives.
  *   - bf16 means IEEE bfloat16 (upper half of a binary32), fp32 is binary32.
  *   - Host-side argument checks fail fast with VT_ERR_INVALID_ARG or
  *     VT_ERR_UNSUPPORTED before anything is launched; a failed launch returns
@@ -321,7 +321,8 @@ vt_status vt_plan_requests(const int32_t* seq_lens, int32_t batch, int32_t* orde
  * page id outside [0, num_pages) takes no part (VT_DEV_BAD_PAGE): the rows are the attention
  * over the request's other pages, zero with lse = -inf where none is left.  Pool slots behind
  * a request's last token are never used, whatever they hold; K and V of the tokens a request
- * has must be finite.  Scores, softmax statistics and accumulators are fp32; the weights are
+ * has, and the scaled scores, must be finite (a query row that is not spoils its own results
+ * only).  out and lse may not overlap the inputs.  Scores, softmax statistics and accumulators are fp32; the weights are
  * rounded once to bf16 for their product with V.
  * Head shapes: (64, 64) and (128, 128), Hq/Hkv <= 8.  Pool strides as everywhere, and not 0
  * for a dimension of more than one entry.

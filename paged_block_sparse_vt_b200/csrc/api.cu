@@ -317,7 +317,7 @@ vt_status attend_common(const vt_paged_kv* kv, int batch, int Hq, const void* q,
   if (pt_stride < 1 || pt_stride > VT_MAX_PAGES_PER_REQUEST)
     return fail(VT_ERR_UNSUPPORTED, "pt_stride %lld outside [1, %d]", (long long)pt_stride,
                 VT_MAX_PAGES_PER_REQUEST);
-  if (!std::isfinite(sm_scale) || !(sm_scale > 0.0f))
+  if (!std::isfinite(sm_scale * kLog2e) || !(sm_scale > 0.0f))
     return fail(VT_ERR_INVALID_ARG, "sm_scale must be positive and finite");
   if (!aligned16(q)) return fail(VT_ERR_UNSUPPORTED, "q not 16-byte aligned");
   *p = AttendParams{};

@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = !SHARED && d.whole;
       const int64_t orow = (int64_t)(d.tok0 + tok) * Hq + d.h * p.G + head_row;
       const float mc = m == -INFINITY ? -INFINITY : m * c;
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
       const int rows = min(32, n_tok * p.G - (warp & 3) * 32);  // of this warp, the valid ones
       // each lane's eight rows r0, r0 + 4, .. in the stores: byte offsets from the result's base
       const int r0 = lane >> 3, piece = lane & 7;
@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma::tmem_landed(o[0]);
           umma::tmem_landed(o[1]);
         }
-        if (!(l > 0.0f)) {
+        if (l == 0.0f) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e >> 4][e & 15] = 0u;
         }
@@ -977,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma::tmem_landed(o[0]);
                 umma::tmem_landed(o[1]);
               }
-              if (!(l > 0.0f)) {
+              if (l == 0.0f) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e >> 4][e & 15] = 0u;
               }
@@ -1014,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!whole)
           *reinterpret_cast<float2*>(base_out + row_at + D * 4) = make_float2(mc, l);
         else if (p.lse)
-          p.lse[orow] = l > 0.0f ? mc * kLn2 + logf(l) : -INFINITY;
+          p.lse[orow] = l != 0.0f ? mc * kLn2 + logf(l) : -INFINITY;
       }
     }
   }
@@ -1054,11 +1054,11 @@ struct Join {
     for (int e = 0; e < E; ++e) o[e] = o[e] * fa + x[e] * fb;
   }
   __device__ __forceinline__ void write(__nv_bfloat16* out, float* lse, int64_t row, int lane) {
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(out + row * D) + lane * (E / 2);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) dst[e] = pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
-    if (lse && lane == 0) lse[row] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+    if (lse && lane == 0) lse[row] = l != 0.0f ? m * kLn2 + logf(l) : -INFINITY;
   }
 };
 
@@ -1192,11 +1192,11 @@ __global__ void __launch_bounds__(kJoinThreads)
       join(piece);
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (int64_t)orow * D) + lane * (E / 2);
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) dst[e] = pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
-  if (p.lse && lane == 0) p.lse[orow] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+  if (p.lse && lane == 0) p.lse[orow] = l != 0.0f ? m * kLn2 + logf(l) : -INFINITY;
 }
 
 // ---- host -----------------------------------------------------------------------------------

@@ -57,6 +57,7 @@ _COMMON = [
     ({}, dict(sm_scale=-0.1), INV),
     ({}, dict(sm_scale=float("inf")), INV),
     ({}, dict(sm_scale=float("nan")), INV),
+    ({}, dict(sm_scale=3e38), INV),             # times log2 e it leaves fp32
     ({}, dict(q=None), INV),
     ({}, dict(q=FAKE + 0x200008), UNS),
     ({}, dict(page_table=None), INV),

@@ -1,5 +1,9 @@
 """vt_prefill against the definition in 64 bits: head shapes, lengths around the tiles' edges,
 contexts, layouts and strides, rows that are left alone, and what it reports."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -8,6 +12,7 @@ from cache_cases import make_cache, make_pools, make_q, scale_of, starts
 from cache_ref import attend_ref, check_attend, pages_of
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 HEADS = [(1, 1, 64), (2, 1, 128), (6, 2, 64), (4, 1, 128), (10, 2, 128), (12, 2, 64), (7, 1, 128),
          (16, 2, 128), (8, 8, 64)]  # Hq, Hkv, D: every group size from 1 to 8
@@ -88,6 +93,50 @@ def test_rising_scores_move_the_maximum_in_every_tile():
     q = q.abs()
     out, lse, _ = run(q, k, v, table, seq, q_lens)
     check_attend(out, lse, attend_ref(q, k, v, table, seq, q_lens, scale_of(64)))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_query_row_spoils_only_itself(bad):
+    q_lens, ctx = [70, 200], [300, 900]
+    q, k, v, table, seq = case(q_lens, ctx, 6, 2, 64)
+    ref = attend_ref(q, k, v, table, seq, q_lens, scale_of(64))
+    q[5, 1, 7] = q[150, 4, 0] = bad
+    out, lse, st = run(q, k, v, table, seq, q_lens)
+    assert st == 0
+    keep = torch.ones(270, 6, dtype=torch.bool, device="cuda")
+    keep[5, 1] = keep[150, 4] = False
+    assert bool(torch.isnan(out[~keep]).any(1).all())
+    check_attend(out[keep], lse[keep], tuple(x[keep] for x in ref))
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 3.0])
+def test_scales(scale):
+    q_lens, ctx = [40, 150], [500, 0]
+    q, k, v, table, seq = case(q_lens, ctx, 4, 1, 128)
+    out, lse = vt.vt_prefill(q, k, v, table, seq, starts(q_lens), scale)
+    check_attend(out, lse, attend_ref(q, k, v, table, seq, q_lens, scale))
+
+
+def test_captured_by_a_process_that_never_called_it():
+    """The first call of a process inside a stream capture."""
+    code = """if True:
+        import torch, paged_block_sparse_vt_b200 as vt
+        i32 = dict(dtype=torch.int32, device="cuda")
+        k = torch.randn(8, 16, 1, 64, device="cuda", dtype=torch.bfloat16)
+        q = torch.randn(20, 2, 64, device="cuda", dtype=torch.bfloat16)
+        table, seq = torch.arange(8, **i32).view(1, 8), torch.tensor([100], **i32)
+        start, out = torch.tensor([0, 20], **i32), torch.zeros_like(q)
+        vt.load_library()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            vt.vt_prefill(q, k, k, table, seq, start, 0.1, out=out)
+        g.replay()
+        want, _ = vt.vt_prefill(q, k, k, table, seq, start, 0.1)
+        assert torch.equal(out, want) and float(out.abs().sum()) > 0
+    """
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120,
+                       cwd=ROOT)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_rows_behind_the_last_prompt_are_left_alone():
