@@ -8,12 +8,17 @@
 //
 // One step, for either row tile t, with everything fp32 but the operands of the products:
 //   S_t = Q_t K^T                (tcgen05, 128 x 128 in tensor memory)
-//   m   = max(m, max_j S_t[r, j]), l = l f + sum_j p_j, p_j = 2^(c S_t[r, j] - c m), c = scale log2 e
+//   p_j = 2^(c S_t[r, j] - ref), l = l + sum_j p_j      with c = scale log2 e
 //   P_t = bf16(p)                (over the columns of S_t)
-//   O_t = O_t f + P_t V          (tcgen05, P_t read from tensor memory)
-// A warpgroup has one tile, a thread one row, so no sum or maximum crosses lanes.  f = 1 unless
-// the maximum rose: O_t is rescaled only when it rose by more than 2^kLazy since the last time
-// (until then p <= 2^kLazy, which loses nothing in bf16 or in fp32).
+//   O_t = O_t + P_t V            (tcgen05, P_t read from tensor memory)
+// A warpgroup has one tile, a thread one row, so no sum crosses lanes.  The reference need not be
+// the largest score: out = O / l does not depend on it, and a weight of 2^50 keeps as many bits in
+// bf16 and fp32 as one of 1.  So a step takes no maximum.  Its reference is that of the first
+// tile's maximum, and where a tile's weights sum to 2^kLift or more, the next step first raises
+// the reference by that sum's exponent and scales O_t and l.  Only a half whose weights sum to
+// kFar or more is done again, with its maximum; and so is, from the start, a tile of which some
+// keys are hidden.  The weights of a half of the keys are handed over as they are done, so that
+// their product runs beside the other half's exponentials.
 //
 // One warp loads: K and V tiles alternate in a ring of shared-memory stages, each of them 8
 // pages by TMA in 128-byte swizzled boxes of 16 tokens x 64 dims, straight from the pools through
@@ -48,7 +53,9 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kDescs = 4;       // items described ahead
 constexpr int kBadRing = 16;    // key tiles whose page checks are kept (> tiles in flight)
 constexpr int kPlan = 1024;     // entries of the cost table in shared memory
-constexpr float kLazy = 8.0f;
+constexpr float kLazy = 8.0f;     // bits by which a known maximum may pass the reference
+constexpr int kLift = 12;         // bits of a tile's sum from which on the reference moves
+constexpr float kFar = 0x1p100f;  // a sum of weights that is not used any more
 constexpr int kPagesTile = kKeys / kPage;
 constexpr int kSoftWarps = 8;
 constexpr int kStage = 32 * 128;  // a softmax warp's staging: 128 bytes of each of its rows
@@ -100,7 +107,7 @@ constexpr int kRowF = D + 4;
 struct Shared {
   Desc desc[kDescs];
   int bad[kBadRing];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2][2], o_full[2], desc_full[kDescs],
+  uint64_t q_full, q_empty, s_full[2], p_ready[2][2], a_done[2], o_full[2], desc_full[kDescs],
       desc_empty[kDescs], kv_full[8], kv_empty[8], drain;
   uint32_t tmem;
   int abort;
@@ -444,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma::mbar_init(smem_u32(&sh.s_full[t]), 1);
       umma::mbar_init(smem_u32(&sh.p_ready[t][0]), 4);
       umma::mbar_init(smem_u32(&sh.p_ready[t][1]), 4);
+      umma::mbar_init(smem_u32(&sh.a_done[t]), 1);
       umma::mbar_init(smem_u32(&sh.o_full[t]), 1);
     }
     for (int i = 0; i < kDescs; ++i) {
@@ -764,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!go) break;
             umma::fence_after_sync();
             values(t, vst, 0, j > j0 + 1);
+            umma::commit(smem_u32(&sh.a_done[t]));
             go = wait(smem_u32(&sh.p_ready[t][1]), p_phase[t], abort_flag);
             if (!go) break;
             umma::fence_after_sync();
@@ -799,10 +808,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tm_row = tm + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
     const uint32_t tm_s = tm_row + t * kKeys, tm_o = tm_row + 2 * kKeys + t * D;
-    const float c = p.qscale, lazy = kLazy / c;
+    const float c = p.qscale;
     const int Hq = p.Hkv * p.G;
     const int tok_row = row / p.G, head_row = row - tok_row * p.G;
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, a_phase = 0;
     int n_tile = 0;
     for (int n_desc = 0;; ++n_desc) {
       const int di = n_desc % kDescs;
@@ -816,15 +825,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         n_tile += d.j1 - d.j0;
         continue;
       }
-      const bool active = (warp & 3) * 32 < n_tok * p.G;
+      const bool active = (warp & 3) * 32 < n_tok * p.G, mine = row < n_tok * p.G;
       const int tok = t * tpt + min(tok_row, n_tok - 1);
       const int vis = d.vis0 + tok * d.step;
       const int vis_warp = d.vis0 + (t * tpt + min((warp & 3) * 32 / p.G, n_tok - 1)) * d.step;
       const int n_pages = (d.kv_len + kPage - 1) / kPage;
       const int gap = n_pages * kPage - d.kv_len;   // zero rows ahead of the last page's tokens
-      float m = -INFINITY, l = 0.0f;
+      // ref: the reference of this row's weights (base 2), l: their sum, lift: what the next tile
+      // adds to the reference
+      float ref = -INFINITY, l = 0.0f, lift = 0.0f;
+      auto move = [&](float to, bool with_o) {
+        const float f = ref == -INFINITY ? 0.0f : ex2(ref - to);
+        ref = to;
+        l *= f;
+        if (with_o) {
+#pragma unroll 1
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t o[16];
+            umma::tmem_ld16(tm_o + 16 * i, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            umma::tmem_st16_async(tm_o + 16 * i, o);
+          }
+        }
+      };
+      // half of the keys have their weights: the product with their values can start
+      auto hand_over = [&](int h) {
+        umma::tmem_wait_st();
+        umma::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(smem_u32(&sh.p_ready[t][h]));
+      };
       bool ok = true;
-      for (int j = d.j0; j < d.j1; ++j, ++n_tile) {
+      for (int j = d.j0; j < d.j1; ++j, ++n_tile, a_phase ^= 1) {
         ok = wait(smem_u32(&sh.s_full[t]), s_phase, abort_flag);
         if (!ok) break;
         s_phase ^= 1;
@@ -833,92 +866,124 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bad = (uint32_t)*(volatile int*)&sh.bad[n_tile % kBadRing];
           const int slot0 = j * kKeys;
           const bool masked = slot0 + kKeys > vis_warp || bad;
-          if (masked) {  // what a row may not see becomes -inf in place
-            RowMask rm;
-            const int last0 = (n_pages - 1) * kPage;  // the last page's first slot
-            rm.lim = (vis > last0 ? vis + gap : vis) - slot0;
-            rm.hole0 = last0 - slot0;
-            rm.hole1 = rm.hole0 + gap;
-            rm.bad = bad;
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              uint32_t s[32];
-              umma::tmem_ld32_async(tm_s + 32 * i, s);
-              const uint32_t ms = rm.word(i);
-              umma::tmem_wait_ld();
-              umma::tmem_landed(s);
+          // The usual tile: nothing to hide, and the reference serves as it is.
+          int slow = 0;  // the first half that is still to be done: 0, 1, or 2 for none
+          if (!masked && __all_sync(kFull, !mine || ref > -INFINITY)) {
+            if (__any_sync(kFull, mine && lift > 0.0f)) move(ref + lift, true);
+            lift = 0.0f;
+            const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
+            uint32_t s[2][32];
+            float tile_sum = 0.0f;
+            umma::tmem_ld32_async(tm_s, s[0]);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(ms >> e & 1u)) s[e] = __float_as_uint(-INFINITY);
-              umma::tmem_st32_async(tm_s + 32 * i, s);
+            for (int h = 0; h < 2; ++h) {
+              if (slow < h) continue;
+              uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+              uint32_t pk[32];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                umma::tmem_wait_ld();
+                umma::tmem_landed(s[i]);
+                if (h + i < 2) umma::tmem_ld32_async(tm_s + 64 * h + 32 * (i + 1), s[i ^ 1]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const uint64_t x = exp2_unit(fma2(
+                      pair(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), c2,
+                      ref2));
+                  sum[e & 1] = add2(sum[e & 1], x);
+                  pk[16 * i + e] = pack2(x);
+                }
+              }
+              const float half_sum = total2(sum[0], sum[1]);
+              if (__any_sync(kFull, mine && !(half_sum < kFar))) {
+                umma::tmem_wait_ld();  // (a load may be in flight into these registers)
+                umma::tmem_landed(s[0]);
+                continue;
+              }
+              umma::tmem_st32_async(tm_s + 32 * h, pk);  // (over scores that were read)
+              l += half_sum;
+              tile_sum += half_sum;
+              hand_over(h);
+              slow = h + 1;
             }
-            umma::tmem_wait_st();
+            // its exponent, from 2^kLift on
+            if (tile_sum >= (float)(1 << kLift))
+              lift = (float)((int)(__float_as_uint(tile_sum) >> 23) - 127);
+            if (slow == 1) {  // the first half is in O, or about to be: it moves with the rest
+              if (!wait(smem_u32(&sh.a_done[t]), a_phase, abort_flag)) {
+                ok = false;
+                break;
+              }
+              umma::fence_after_sync();
+            }
           }
-          // The scores are read twice, for the maximum and for the weights: a row of 128 does not
-          // stay in registers without spills, and a second read costs 32 cycles per 32 columns.
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          {
-            uint32_t s[4][32];
+          if (slow < 2) {
+            if (masked) {  // what a row may not see becomes -inf in place
+              RowMask rm;
+              const int last0 = (n_pages - 1) * kPage;  // the last page's first slot
+              rm.lim = (vis > last0 ? vis + gap : vis) - slot0;
+              rm.hole0 = last0 - slot0;
+              rm.hole1 = rm.hole0 + gap;
+              rm.bad = bad;
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) {
+                uint32_t s[32];
+                umma::tmem_ld32_async(tm_s + 32 * i, s);
+                const uint32_t ms = rm.word(i);
+                umma::tmem_wait_ld();
+                umma::tmem_landed(s);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) umma::tmem_ld32_async(tm_s + 32 * i, s[i]);
-            umma::tmem_wait_ld();
+                for (int e = 0; e < 32; ++e)
+                  if (!(ms >> e & 1u)) s[e] = __float_as_uint(-INFINITY);
+                umma::tmem_st32_async(tm_s + 32 * i, s);
+              }
+              umma::tmem_wait_st();
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int i = slow; i < 2; ++i) {
+              uint32_t s0[32], s1[32];
+              umma::tmem_ld32_async(tm_s + 64 * i, s0);
+              umma::tmem_ld32_async(tm_s + 64 * i + 32, s1);
+              umma::tmem_wait_ld();
+              umma::tmem_landed(s0);
+              umma::tmem_landed(s1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) umma::tmem_landed(s[i]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int e = 0; e < 32; e += 8)
+              for (int e = 0; e < 32; e += 4)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(s[i][e + k]),
-                                             __uint_as_float(s[i][e + 4 + k])));
-          }
-          uint32_t s[2][32];
-          umma::tmem_ld32_async(tm_s, s[0]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (__any_sync(kFull, top > m + lazy || (m == -INFINITY && top > m))) {
-            const float mn = fmaxf(m, top);
-            const float f = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
-            m = mn;
-            l *= f;
-            if (j > d.j0) {
+                  mx[k] =
+                      fmaxf(mx[k], fmaxf(__uint_as_float(s0[e + k]), __uint_as_float(s1[e + k])));
+            }
+            const float top =
+                fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c, ref + lift);
+            lift = 0.0f;
+            if (__any_sync(kFull, mine && (top > ref + kLazy || (ref == -INFINITY && top > ref))))
+              move(fmaxf(ref, top), j > d.j0 || slow == 1);
+            const float at = ref == -INFINITY ? 0.0f : ref;
+            const uint64_t c2 = pair(c, c), ref2 = pair(-at, -at);
 #pragma unroll 1
-              for (int i = 0; i < D / 16; ++i) {
-                uint32_t o[16];
-                umma::tmem_ld16(tm_o + 16 * i, o);
+            for (int h = slow; h < 2; ++h) {
+              uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll 1
+              for (int i = 0; i < 2; ++i) {
+                uint32_t s[32], pk[16];
+                umma::tmem_ld32_async(tm_s + 64 * h + 32 * i, s);
+                umma::tmem_wait_ld();
+                umma::tmem_landed(s);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                umma::tmem_st16_async(tm_o + 16 * i, o);
+                for (int e = 0; e < 16; ++e) {
+                  const uint64_t x = exp2_unit(fma2(
+                      pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, ref2));
+                  sum[e & 1] = add2(sum[e & 1], x);
+                  pk[e] = pack2(x);
+                }
+                umma::tmem_st16_async(tm_s + 32 * h + 16 * i, pk);
               }
+              l += total2(sum[0], sum[1]);
+              hand_over(h);
             }
           }
-          const float mc = m == -INFINITY ? 0.0f : m * c;
-          const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
-          uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            umma::tmem_wait_ld();
-            umma::tmem_landed(s[i & 1]);
-            if (i < 3) umma::tmem_ld32_async(tm_s + 32 * (i + 1), s[(i + 1) & 1]);
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              uint64_t x = fma2(pair(__uint_as_float(s[i & 1][2 * e]),
-                                     __uint_as_float(s[i & 1][2 * e + 1])),
-                                c2, mc2);
-              x = exp2_unit(x);
-              sum[e & 1] = add2(sum[e & 1], x);
-              pk[e] = pack2(x);
-            }
-            umma::tmem_st16_async(tm_s + 16 * i, pk);  // (over scores that were read)
-            if (i & 1) {  // half of the keys: the product with their values can start
-              umma::tmem_wait_st();
-              umma::fence_before_sync();
-              __syncwarp();
-              if (lane == 0) umma::mbar_arrive(smem_u32(&sh.p_ready[t][i >> 1]));
-            }
-          }
-          l += total2(sum[0], sum[1]);
         } else if (lane == 0) {
           umma::mbar_arrive(smem_u32(&sh.p_ready[t][0]));
           umma::mbar_arrive(smem_u32(&sh.p_ready[t][1]));
@@ -936,7 +1001,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // row it would touch 32 of them.
       const bool whole = !SHARED && d.whole;
       const int64_t orow = (int64_t)(d.tok0 + tok) * Hq + d.h * p.G + head_row;
-      const float mc = m == -INFINITY ? -INFINITY : m * c;
       const float inv = l != 0.0f ? 1.0f / l : 0.0f;
       const int rows = min(32, n_tok * p.G - (warp & 3) * 32);  // of this warp, the valid ones
       // each lane's eight rows r0, r0 + 4, .. in the stores: byte offsets from the result's base
@@ -1012,9 +1076,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane < rows) {
         if (!whole)
-          *reinterpret_cast<float2*>(base_out + row_at + D * 4) = make_float2(mc, l);
+          *reinterpret_cast<float2*>(base_out + row_at + D * 4) = make_float2(ref, l);
         else if (p.lse)
-          p.lse[orow] = l != 0.0f ? mc * kLn2 + logf(l) : -INFINITY;
+          p.lse[orow] = l != 0.0f ? ref * kLn2 + logf(l) : -INFINITY;
       }
     }
   }
