@@ -11,7 +11,10 @@
 // CTA counts its contiguous share, the counts are exchanged over distributed shared memory, and
 // a second walk over the share (now in L1/L2) hands out the ranks.  A grid-wide scan would take
 // a second launch for the same exchange, and a single CTA reads 1 MB of counts (a pool of 262144
-// pages) at one SM's rate.  What has to be copied then goes over the whole GPU in a second launch.
+// pages) at one SM's rate.  What has to be copied then goes over the whole GPU in a second launch,
+// a side (K or V) of a page per CTA: 6.0 TB/s, 0.92 of a plain copy's rate, for 6000 pages of 64 KB.
+// Small calls are bound by their launches: a fork of 4 requests of a pool of 1000 pages takes two
+// of ~5 us each on the GPU, and 13 us on the host.
 #include "common.cuh"
 #include "pages.cuh"
 
