@@ -1166,8 +1166,9 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 // Shared prefixes: a warp joins one row, the pieces of its group's prefix and of its own pages.
-// Which shares hold a piece is worked out for 32 of them at a time, a lane each, and their m and l
-// are read at once: one after the other, a prefix of 18 pieces took 18 trips to memory (23 us).
+// The time is a chain of trips to memory (10 us for 32 samples of a prompt), so it has few links:
+// which shares hold a piece is worked out a lane each, all their m and l are read at once, and the
+// rows eight at a time.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
     join_rows_kernel(const AttendParams p, const Work w) {
@@ -1178,93 +1179,98 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (orow >= p.B * Hq) return;
   const int b = orow / Hq, hq = orow - b * Hq;
   const int h = hq / p.G, g_row = hq - h * p.G;
+  const int g = group_of(p, b);
+  Unit own{}, un{};
+  if (g >= 0) {  // (inputs, which the kernel before does not write)
+    own = load_unit<true>(p, p.n_groups + b);
+    un = load_unit<true>(p, g);
+  }
+  const int t = (b - un.tok0) / (2 * tpt), i = (b - un.tok0) - t * 2 * tpt;
+  const int r = i / tpt * kTile + i % tpt * p.G + g_row;  // the row within the prefix's item
+  const int64_t a_in = h * cost_before(un, tpt, unit_items(un, tpt)) + cost_before(un, tpt, t);
+  const int64_t a_cost = un.n > 0 ? item_cost(un, tpt, t) : 0, b_cost = own_cost(own);
+  const int wt = un.n > 0 ? item_weight(un, tpt, t) : 1;
+  const int tiles = un.n > 0 ? (item_keys(un, tpt, t) + kKeys - 1) / kKeys : 0;
+  const int n_pages = own_pages(own);
   wait_for_previous();
   const Line tl = w.lines[0], ol = w.lines[1];
-  const int64_t own_at = w.line[p.n_groups + b];
-  if (tl.total < 0) return;
-  const int g = group_of(p, b);
-  if (g < 0) return;
-  const Unit own = load_unit<true>(p, p.n_groups + b), un = load_unit<true>(p, g);
+  const int64_t b_pos = w.line[p.n_groups + b] + h * b_cost;
+  const int64_t a_pos = (g >= 0 ? w.line[g] : 0) + a_in;
+  if (tl.total < 0 || g < 0) return;
+  // the shares [a0, a1) and [b0, b1) may hold pieces
+  int a0 = 0, a1 = 0, b0 = 0, b1 = 0;
+  if (!own.bad && un.n > 0) {
+    a0 = share_of(tl, a_pos);
+    a1 = share_of(tl, a_pos + a_cost - 1) + 1;
+  }
+  if (!own.bad && own.kv_len > 0) {
+    b0 = share_of(ol, b_pos);
+    b1 = share_of(ol, b_pos + b_cost - 1) + 1;
+  }
   float o[E], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  // joins the pieces that the lanes name (NULL: none)
-  auto join = [&](const float* piece) {
-    const float2 ml = piece ? __ldcg(reinterpret_cast<const float2*>(piece + D))
-                            : make_float2(-INFINITY, 0.0f);
-    float top = fmaxf(m, ml.x);
+#pragma unroll 1
+  for (; a0 < a1 || b0 < b1; a0 += 32, b0 += 32) {
+    // this lane's piece of either kind, NULL none
+    const float *pa = nullptr, *pb = nullptr;
+    if (a0 + lane < a1) {
+      const int j0 = cut_tile(share_begin(tl, a0 + lane) - a_pos, a_cost, wt, tiles);
+      const int j1 = cut_tile(share_begin(tl, a0 + lane + 1) - a_pos, a_cost, wt, tiles);
+      if (j0 < j1)
+        pa = j0 == 0 ? w.first + (int64_t)orow * kRowF<D>
+                     : w.part + ((int64_t)(a0 + lane) * 2 * kTile + r) * kRowF<D>;
+    }
+    if (b0 + lane < b1) {
+      const int i0 = own_cut(share_begin(ol, b0 + lane) - b_pos, n_pages);
+      const int i1 = own_cut(share_begin(ol, b0 + lane + 1) - b_pos, n_pages);
+      if (i0 < i1)
+        pb = i0 == 0 ? w.first + ((int64_t)p.B * Hq + orow) * kRowF<D>
+                     : w.own + ((int64_t)(b0 + lane) * 8 + g_row) * kRowF<D>;
+    }
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    const float2 ma = pa ? __ldcg(reinterpret_cast<const float2*>(pa + D)) : none;
+    const float2 mb = pb ? __ldcg(reinterpret_cast<const float2*>(pb + D)) : none;
+    float top = fmaxf(m, fmaxf(ma.x, mb.x));
 #pragma unroll
     for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
     const float keep = m == -INFINITY ? 0.0f : exp2f(m - top);
-    const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
-    float sum = ml.y * f;
+    const float fa = ma.x == -INFINITY ? 0.0f : exp2f(ma.x - top);
+    const float fb = mb.x == -INFINITY ? 0.0f : exp2f(mb.x - top);
+    float sum = ma.y * fa + mb.y * fb;
 #pragma unroll
     for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
     l = l * keep + sum;
     m = top;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] *= keep;
-    for (uint32_t left = __ballot_sync(kFull, piece != nullptr); left;) {
-      constexpr int kAtOnce = 4;
-      float x[kAtOnce][E], fx[kAtOnce];
+    uint64_t left = __ballot_sync(kFull, pa != nullptr) |
+                    (uint64_t)__ballot_sync(kFull, pb != nullptr) << 32;
+    while (left) {
+      constexpr int kAtOnce = 8;
+      float x[kAtOnce][E], f[kAtOnce];
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
-        const int src = left ? __ffs(left) - 1 : 0;
-        const float* r = reinterpret_cast<const float*>(
-            __shfl_sync(kFull, reinterpret_cast<unsigned long long>(piece), src));
-        fx[k] = __shfl_sync(kFull, f, src);
         const bool has = left != 0;
+        const int src = has ? __ffsll((long long)left) - 1 : 0;
         left &= left - 1;
+        const float* mine = src < 32 ? pa : pb;
+        const float* row = reinterpret_cast<const float*>(
+            __shfl_sync(kFull, reinterpret_cast<unsigned long long>(mine), src & 31));
+        f[k] = __shfl_sync(kFull, src < 32 ? fa : fb, src & 31);
+        if (!has) f[k] = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
-          const float2 v = has ? __ldcg(reinterpret_cast<const float2*>(r + lane * E + e))
+          const float2 v = has ? __ldcg(reinterpret_cast<const float2*>(row + lane * E + e))
                                : make_float2(0.0f, 0.0f);
           x[k][e] = v.x;
           x[k][e + 1] = v.y;
         }
-        if (!has) fx[k] = 0.0f;
       }
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k)
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(x[k][e], fx[k], o[e]);
-    }
-  };
-  if (!own.bad && un.n > 0) {  // the pieces of the group's prefix
-    const int t = (b - un.tok0) / (2 * tpt), i = (b - un.tok0) - t * 2 * tpt;
-    const int r = i / tpt * kTile + i % tpt * p.G + g_row;  // the row within the item
-    const int64_t cost = item_cost(un, tpt, t);
-    const int64_t pos = w.line[g] + h * cost_before(un, tpt, unit_items(un, tpt)) +
-                        cost_before(un, tpt, t);
-    const int wt = item_weight(un, tpt, t);
-    const int tiles = (item_keys(un, tpt, t) + kKeys - 1) / kKeys;
-    for (int c0 = share_of(tl, pos); c0 < tl.n && share_begin(tl, c0) < pos + cost; c0 += 32) {
-      const int c = c0 + lane;
-      const float* piece = nullptr;
-      if (c < tl.n) {
-        const int64_t x0 = share_begin(tl, c) - pos, x1 = share_begin(tl, c + 1) - pos;
-        const int j0 = cut_tile(x0, cost, wt, tiles), j1 = cut_tile(x1, cost, wt, tiles);
-        if (x0 < cost && j0 < j1)
-          piece = j0 == 0 ? w.first + (int64_t)orow * kRowF<D>
-                          : w.part + ((int64_t)c * 2 * kTile + r) * kRowF<D>;
-      }
-      join(piece);
-    }
-  }
-  if (!own.bad && own.kv_len > 0) {  // and those of its own pages
-    const int n_pages = own_pages(own);
-    const int64_t cost = own_cost(own), pos = own_at + h * cost;
-    for (int c0 = share_of(ol, pos); c0 < ol.n && share_begin(ol, c0) < pos + cost; c0 += 32) {
-      const int c = c0 + lane;
-      const float* piece = nullptr;
-      if (c < ol.n) {
-        const int64_t x0 = share_begin(ol, c) - pos, x1 = share_begin(ol, c + 1) - pos;
-        const int i0 = own_cut(x0, n_pages), i1 = own_cut(x1, n_pages);
-        if (x0 < cost && i0 < i1)
-          piece = i0 == 0 ? w.first + ((int64_t)p.B * Hq + orow) * kRowF<D>
-                          : w.own + ((int64_t)c * 8 + g_row) * kRowF<D>;
-      }
-      join(piece);
+        for (int e = 0; e < E; ++e) o[e] = fmaf(x[k][e], f[k], o[e]);
     }
   }
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
