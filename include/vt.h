@@ -448,7 +448,8 @@ vt_status vt_fork_requests(const vt_paged_kv* kv, const vt_page_books* books,
  * past 16 pt_stride tokens is left out (VT_DEV_BAD_LEN); a row listed twice grows by its first
  * entry (VT_DEV_BAD_REQ).  With f free pages, an entry gets its pages if the pages that the
  * entries up to and including it need are at most f; otherwise it is left as it was
- * (VT_DEV_NO_PAGE).  An entry that needs no page is always served.
+ * (VT_DEV_NO_PAGE).  An entry that needs no page is always served.  workspace: as for
+ * vt_fork_requests; lists of up to 2048 entries use none (NULL will do).
  */
 vt_status vt_extend_requests(const vt_page_books* books, int64_t num_pages,
                              const int32_t* requests, const int32_t* tokens, int32_t n,

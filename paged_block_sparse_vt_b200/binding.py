@@ -745,7 +745,9 @@ def vt_extend_requests(page_table, seq_lens, refs, requests, tokens, status=None
     books = _books(page_table, seq_lens, refs, status, dev)
     n, a, b = _lists(dev, requests, tokens, ("requests", "tokens"))
     pages = refs.numel()
-    workspace, ws, ws_bytes = _page_ws(lib, workspace, pages, n, dev)
+    ws, ws_bytes = None, 0
+    if n > 2048:  # (shorter lists use none)
+        workspace, ws, ws_bytes = _page_ws(lib, workspace, pages, n, dev)
     _device_call(lib.vt_extend_requests, "vt_extend_requests", dev, books, pages, a, b, n, ws,
                  ws_bytes)
 

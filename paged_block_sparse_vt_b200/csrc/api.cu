@@ -459,9 +459,11 @@ PageListParams list_params(const vt_page_books* b, int64_t num_pages, const int3
   p.sources = sources;
   p.targets = targets;
   p.n = n;
-  p.len = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + page_workspace(num_pages, n).list);
-  p.need = p.len + n;
-  p.base = p.need + n;
+  if (ws) {
+    p.len = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + page_workspace(num_pages, n).list);
+    p.need = p.len + n;
+    p.base = p.need + n;
+  }
   return p;
 }
 
@@ -693,8 +695,10 @@ vt_status vt_extend_requests(const vt_page_books* books, int64_t num_pages,
   if (n < 0) return fail(VT_ERR_INVALID_ARG, "n < 0");
   if (n == 0) return ok();
   if (!requests || !tokens) return fail(VT_ERR_INVALID_ARG, "requests/tokens is NULL");
-  s = check_workspace(workspace, workspace_bytes, page_workspace(num_pages, n).total);
-  if (s != VT_OK) return s;
+  if (n > kListSmem) {
+    s = check_workspace(workspace, workspace_bytes, page_workspace(num_pages, n).total);
+    if (s != VT_OK) return s;
+  }
   const PageListParams p = list_params(books, num_pages, tokens, requests, n, workspace);
   cudaError_t e = launch_extend(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "extend_requests launch");

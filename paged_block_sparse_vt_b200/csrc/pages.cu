@@ -107,7 +107,6 @@ __device__ __forceinline__ Share my_share(int64_t P, int rank) {
 struct Lists {
   int *len, *need, *base;
 };
-constexpr int kListSmem = 2048;
 
 template <bool FORK>
 __device__ int read_list(const PageListParams& p, const Lists& a, int* s_warp) {

@@ -9,6 +9,9 @@
 
 namespace vt {
 
+// Lists of up to this many entries are worked on in shared memory; longer ones in the workspace.
+constexpr int kListSmem = 2048;
+
 struct PoolView {
   __nv_bfloat16* base;
   int64_t s_p, s_t, s_h;
@@ -34,7 +37,8 @@ struct PageListParams {
   const int32_t* sources;
   const int32_t* targets;
   int n;
-  int32_t* len;   // workspace, n each: the entry's length before the call, -1 left out
+  int32_t* len;   // workspace, n each (a growth of up to kListSmem rows: NULL): the entry's length
+                  //   before the call, -1 left out
   int32_t* need;  //   pages it needs
   int32_t* base;  //   pages that the entries before it need
 };

@@ -157,7 +157,8 @@ def test_page_call_refusals(lib):
     assert lib.vt_page_workspace_size(0, 3) == 0 and lib.vt_page_workspace_size(1000, -1) == 0
     for ws, size in ((None, BIG), (FAKE, need - 1), (FAKE + 16, BIG)):
         assert lib.vt_fork_requests(kv, b, FAKE, FAKE, 3, ws, size, None) == INV
-        assert lib.vt_extend_requests(b, 1000, FAKE, FAKE, 3, ws, size, None) == INV
+        # (up to 2048 rows grow without a workspace)
+        assert lib.vt_extend_requests(b, 1000, FAKE, FAKE, 2049, ws, size, None) == INV
     assert lib.vt_compact_pages(kv, b, None, FAKE, None, BIG, None) == INV
     assert lib.vt_compact_pages(kv, b, None, None, FAKE, BIG, None) == INV
     assert lib.vt_compact_pages(kv, b, FAKE + 4, FAKE, FAKE, BIG, None) == UNS
