@@ -86,18 +86,19 @@ def test_flat_and_sharp_scores(gain):
 
 @pytest.mark.parametrize("at", [(70, 198, 300), (10, 140, 210, 390), (127, 128, 255, 256, 511),
                                 (64, 65, 66, 447)])
-def test_scores_that_rise_by_more_than_100_bits_at_once(at):
+@pytest.mark.parametrize("hq,d", [(2, 64), (5, 128)])
+def test_scores_that_rise_by_more_than_100_bits_at_once(at, hq, d):
     """Keys whose scores are 150 bits above all before them, in either half of a step of 128 keys;
     every row's result is the value of the last of them that it sees, to rounding."""
     q_lens, ctx = [300], [260]
-    q, k, v, table, seq = case(q_lens, ctx, 2, 1, 64, poison=False)
+    q, k, v, table, seq = case(q_lens, ctx, hq, 1, d, poison=False)
     k *= 0.3
     page = table[0].long()
     for i, pos in enumerate(at):
         k[page[pos // 16], pos % 16] = 13.0 * (i + 1)      # 64 * 13 / 8 = 104, 150 in base 2
     q = torch.ones_like(q)
     out, lse, _ = run(q, k, v, table, seq, q_lens)
-    check_attend(out, lse, attend_ref(q, k, v, table, seq, q_lens, scale_of(64)))
+    check_attend(out, lse, attend_ref(q, k, v, table, seq, q_lens, scale_of(d)))
 
 
 def test_rising_scores_move_the_maximum_in_every_tile():
