@@ -34,8 +34,8 @@
 //
 // What bounds it: a step of two row tiles takes ~3200 cycles, its products and its exponentials
 // 2048 each; the rest is the chain scores - exponentials - values of a tile, and tensor memory has
-// room for two tiles (512 columns: S and O of 128 each).  A prompt of 8192 tokens (32/8 heads of 128
-// dims) runs at 1160 TFLOP/s, its products alone at 1450.  Code size counts: the rare paths are
+// room for two tiles (512 columns: S and O of 128 each).  A prompt of 8192 tokens (32/8 heads of
+// 128 dims) runs at 1160 TFLOP/s, its products alone at 1450.  Code size counts: the rare paths are
 // loops that are not unrolled, which took a packed batch from 350 to 330 us.
 #include <cuda.h>
 
@@ -51,7 +51,8 @@ namespace vt {
 
 namespace {
 
-constexpr int kThreads = 384;   // two softmax warpgroups, and one with the loading and product warps
+// two softmax warpgroups, and one with the loading and the product warp
+constexpr int kThreads = 384;
 // Registers: a softmax thread holds its row of scores, 128 of them, beside the rest; what the
 // third warpgroup gives up goes to the other two (2 * 200 + 104 = 3 * 168, the launch's share).
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
@@ -102,7 +103,7 @@ struct Work {          // the workspace
                        //   2c + 1 begins one; shared prefixes: [ctas][256][D + 4], slot c continues
   float* first;        // shared prefixes: [2][B Hq][D + 4], the rows of items' first pieces:
                        //   prefixes, then own pages
-  float* own;          // shared prefixes: [ctas kWarps][8][D + 4]: rows that a warp's share continues
+  float* own;          // shared prefixes: [ctas kWarps][8][D + 4], rows that a share continues
   int64_t* line;       // shared prefixes: [units] where each unit begins in its line
   Line* lines;         // shared prefixes: the two lines; lines[0].total -1: nothing was done
 };
@@ -558,260 +559,263 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t* line = table0;
   const bool work = total > 0 && cta < tiles_line.n;
   if (warp >= kLoadWarp) {
-  regs_less<kRegsOther>();
-  if (warp == kLoadWarp) {
-    // ---- loading -----------------------------------------------------------------------------
-    if (lane == 0 && !SHARED && w.head) {
-      w.head[2 * cta].valid = 0;
-      w.head[2 * cta + 1].valid = 0;
-    }
-    int n_desc = 0, n_item = 0, n_tile = 0;
-    uint32_t filled = 0;  // stage uses, for the drain behind an abort
-    bool go = true;
-    if (work) {
-      const int64_t x0 = share_begin(tiles_line, cta), x1 = share_begin(tiles_line, cta + 1);
-      int lo = 0, hi = entries - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (line[mid] <= x0) lo = mid; else hi = mid - 1;
+    regs_less<kRegsOther>();
+    if (warp == kLoadWarp) {
+      // ---- loading -----------------------------------------------------------------------------
+      if (lane == 0 && !SHARED && w.head) {
+        w.head[2 * cta].valid = 0;
+        w.head[2 * cta + 1].valid = 0;
       }
-      int u = lo * per;
-      int64_t pos = line[lo];
-      Unit un = load_unit<SHARED>(p, u);
-      int items = unit_items(un, tpt);
-      int64_t head_cost = cost_before(un, tpt, items);
-      while (pos + p.Hkv * head_cost <= x0) {  // x0 < total, so this ends at a unit with items
-        pos += p.Hkv * head_cost;
-        un = load_unit<SHARED>(p, ++u);
-        items = unit_items(un, tpt);
-        head_cost = cost_before(un, tpt, items);
-      }
-      int h = (int)((x0 - pos) / head_cost);
-      pos += h * head_cost;
-      int t = 0;
-      {
-        int a = 0, b = items - 1;
-        while (a < b) {
-          const int mid = (a + b + 1) >> 1;
-          if (cost_before(un, tpt, mid) <= x0 - pos) a = mid; else b = mid - 1;
+      int n_desc = 0, n_item = 0, n_tile = 0;
+      uint32_t filled = 0;  // stage uses, for the drain behind an abort
+      bool go = true;
+      if (work) {
+        const int64_t x0 = share_begin(tiles_line, cta), x1 = share_begin(tiles_line, cta + 1);
+        int lo = 0, hi = entries - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (line[mid] <= x0) lo = mid; else hi = mid - 1;
         }
-        t = a;
-        pos += cost_before(un, tpt, t);
-      }
-      umma::fence_async_smem();  // the table has been read
-      while (go && pos < x1) {
-        const int64_t cost = item_cost(un, tpt, t);
-        const int keys = item_keys(un, tpt, t), wt = item_weight(un, tpt, t);
-        const int tiles = (keys + kKeys - 1) / kKeys;
-        const int j0 = cut_tile(x0 - pos, cost, wt, tiles), j1 = cut_tile(x1 - pos, cost, wt, tiles);
-        if (j0 < j1 || (tiles == 0 && pos >= x0)) {
-          // describe it
-          const int di = n_desc % kDescs;
-          go = wait(smem_u32(&sh.desc_empty[di]), ((n_desc / kDescs) & 1) ^ 1, abort_flag);
-          if (!go) break;
-          const int first = t * 2 * tpt, n_tok = min(un.n - first, 2 * tpt);
-          const bool whole = j0 == 0 && j1 == tiles;
-          if (lane == 0) {
-            Desc d;
-            d.tok0 = un.tok0 + first;
-            d.n_tok = n_tok;
-            d.h = h;
-            d.j0 = j0;
-            d.j1 = j1;
-            d.vis0 = un.vis0 + first * un.step;
-            d.step = un.step;
-            d.kv_len = un.kv_len;
-            d.whole = whole;
-            d.slot = SHARED ? cta : whole ? -1 : 2 * cta + (j0 == 0);
-            sh.desc[di] = d;
-            if (!SHARED && !whole) {
-              Head hd{un.tok0 + first, n_tok, h, j0, j1, tiles, 1, 0};
-              w.head[d.slot] = hd;
-            }
-            umma::mbar_arrive(smem_u32(&sh.desc_full[di]));
+        int u = lo * per;
+        int64_t pos = line[lo];
+        Unit un = load_unit<SHARED>(p, u);
+        int items = unit_items(un, tpt);
+        int64_t head_cost = cost_before(un, tpt, items);
+        while (pos + p.Hkv * head_cost <= x0) {  // x0 < total, so this ends at a unit with items
+          pos += p.Hkv * head_cost;
+          un = load_unit<SHARED>(p, ++u);
+          items = unit_items(un, tpt);
+          head_cost = cost_before(un, tpt, items);
+        }
+        int h = (int)((x0 - pos) / head_cost);
+        pos += h * head_cost;
+        int t = 0;
+        {
+          int a = 0, b = items - 1;
+          while (a < b) {
+            const int mid = (a + b + 1) >> 1;
+            if (cost_before(un, tpt, mid) <= x0 - pos) a = mid; else b = mid - 1;
           }
-          ++n_desc;
-          // its tiles
-          const int n_pages = (un.kv_len + kPage - 1) / kPage;
-          const int last = un.kv_len - kPage * (n_pages - 1);  // tokens on the last page
-          const int32_t* table = p.page_table + (int64_t)un.row * p.pt_stride + un.page0;
-          auto page_id = [&](int j) {  // of lane's page among the four tiles from j
-            const int i = j * kPagesTile + lane;
-            return i < n_pages && j < j1 ? table[i] : -1;
-          };
-          int ids = 0, next = j0 < j1 ? page_id(j0) : 0;
-          for (int j = j0; go && j < j1; ++j, ++n_tile) {
-            if ((j - j0) % 4 == 0) {
-              ids = next;
-              next = page_id(j + 4);
-            }
-            const int mine = ((j - j0) & 3) * kPagesTile + (lane & 7);
-            int id = __shfl_sync(kFull, ids, mine);
-            const int i = j * kPagesTile + (lane & 7);
-            const bool there = i < n_pages;
-            const bool bad = there && (id < 0 || id >= p.kv.num_pages);
-            const uint32_t bads = __ballot_sync(kFull, bad) & 0xffu;
-            // tokens [0, 16), the last page's from a negative one; [16, 32): all zeros
-            int c_tok = i == n_pages - 1 ? last - kPage : 0;
-            if (!there || bad) {
-              id = 0;
-              c_tok = kPage;
-            }
+          t = a;
+          pos += cost_before(un, tpt, t);
+        }
+        umma::fence_async_smem();  // the table has been read
+        while (go && pos < x1) {
+          const int64_t cost = item_cost(un, tpt, t);
+          const int keys = item_keys(un, tpt, t), wt = item_weight(un, tpt, t);
+          const int tiles = (keys + kKeys - 1) / kKeys;
+          const int j0 = cut_tile(x0 - pos, cost, wt, tiles);
+          const int j1 = cut_tile(x1 - pos, cost, wt, tiles);
+          if (j0 < j1 || (tiles == 0 && pos >= x0)) {
+            // describe it
+            const int di = n_desc % kDescs;
+            go = wait(smem_u32(&sh.desc_empty[di]), ((n_desc / kDescs) & 1) ^ 1, abort_flag);
+            if (!go) break;
+            const int first = t * 2 * tpt, n_tok = min(un.n - first, 2 * tpt);
+            const bool whole = j0 == 0 && j1 == tiles;
             if (lane == 0) {
-              sh.bad[n_tile % kBadRing] = (int)bads;
-              if (bads) flag(p.status, VT_DEV_BAD_PAGE);
+              Desc d;
+              d.tok0 = un.tok0 + first;
+              d.n_tok = n_tok;
+              d.h = h;
+              d.j0 = j0;
+              d.j1 = j1;
+              d.vis0 = un.vis0 + first * un.step;
+              d.step = un.step;
+              d.kv_len = un.kv_len;
+              d.whole = whole;
+              d.slot = SHARED ? cta : whole ? -1 : 2 * cta + (j0 == 0);
+              sh.desc[di] = d;
+              if (!SHARED && !whole) {
+                Head hd{un.tok0 + first, n_tok, h, j0, j1, tiles, 1, 0};
+                w.head[d.slot] = hd;
+              }
+              umma::mbar_arrive(smem_u32(&sh.desc_full[di]));
             }
+            ++n_desc;
+            // its tiles
+            const int n_pages = (un.kv_len + kPage - 1) / kPage;
+            const int last = un.kv_len - kPage * (n_pages - 1);  // tokens on the last page
+            const int32_t* table = p.page_table + (int64_t)un.row * p.pt_stride + un.page0;
+            auto page_id = [&](int j) {  // of lane's page among the four tiles from j
+              const int i = j * kPagesTile + lane;
+              return i < n_pages && j < j1 ? table[i] : -1;
+            };
+            int ids = 0, next = j0 < j1 ? page_id(j0) : 0;
+            for (int j = j0; go && j < j1; ++j, ++n_tile) {
+              if ((j - j0) % 4 == 0) {
+                ids = next;
+                next = page_id(j + 4);
+              }
+              const int mine = ((j - j0) & 3) * kPagesTile + (lane & 7);
+              int id = __shfl_sync(kFull, ids, mine);
+              const int i = j * kPagesTile + (lane & 7);
+              const bool there = i < n_pages;
+              const bool bad = there && (id < 0 || id >= p.kv.num_pages);
+              const uint32_t bads = __ballot_sync(kFull, bad) & 0xffu;
+              // tokens [0, 16), the last page's from a negative one; [16, 32): all zeros
+              int c_tok = i == n_pages - 1 ? last - kPage : 0;
+              if (!there || bad) {
+                id = 0;
+                c_tok = kPage;
+              }
+              if (lane == 0) {
+                sh.bad[n_tile % kBadRing] = (int)bads;
+                if (bads) flag(p.status, VT_DEV_BAD_PAGE);
+              }
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-              const int use = 2 * n_tile + kv, st = use % C::STAGES;
-              const uint32_t full = smem_u32(&sh.kv_full[st]);
-              go = go && wait(smem_u32(&sh.kv_empty[st]), ((use / C::STAGES) & 1) ^ 1, abort_flag);
-              if (!go) break;
-              if (lane == 0) umma::mbar_expect_tx(full, C::TILE);
-              __syncwarp();
-              if (lane < kPagesTile * C::HALVES) {
-                const int half = lane / kPagesTile;
-                umma::tma_load_4d(kv_smem + st * C::TILE + half * C::BOX +
-                                      (lane & 7) * (kPage * 128),
-                                  kv ? &v_map : &k_map, half * 64, c_tok, h, id, full);
-              }
-              ++filled;
-              if (kv == 0 && j == j0) {
-                // q goes behind the first K tile: its buffer is free only when the last item's
-                // scores are done
-                go = wait(smem_u32(&sh.q_empty), (n_item & 1) ^ 1, abort_flag);
+              for (int kv = 0; kv < 2; ++kv) {
+                const int use = 2 * n_tile + kv, st = use % C::STAGES;
+                const uint32_t full = smem_u32(&sh.kv_full[st]);
+                go = go &&
+                     wait(smem_u32(&sh.kv_empty[st]), ((use / C::STAGES) & 1) ^ 1, abort_flag);
                 if (!go) break;
-                const int tiles_q = n_tok > tpt ? 2 : 1;
-                if (lane == 0) {
-                  const uint32_t bar = smem_u32(&sh.q_full);
-                  umma::mbar_expect_tx(bar, p.G * tpt * 128 * C::HALVES * tiles_q);
-                  for (int tt = 0; tt < tiles_q; ++tt)
-                    for (int half = 0; half < C::HALVES; ++half)
-                      umma::tma_load_3d(q_smem + tt * C::TILE + half * C::BOX, &q_map, half * 64,
-                                        h * p.G, un.tok0 + first + tt * tpt, bar);
+                if (lane == 0) umma::mbar_expect_tx(full, C::TILE);
+                __syncwarp();
+                if (lane < kPagesTile * C::HALVES) {
+                  const int half = lane / kPagesTile;
+                  umma::tma_load_4d(kv_smem + st * C::TILE + half * C::BOX +
+                                        (lane & 7) * (kPage * 128),
+                                    kv ? &v_map : &k_map, half * 64, c_tok, h, id, full);
                 }
-                ++n_item;
+                ++filled;
+                if (kv == 0 && j == j0) {
+                  // q goes behind the first K tile: its buffer is free only when the last item's
+                  // scores are done
+                  go = wait(smem_u32(&sh.q_empty), (n_item & 1) ^ 1, abort_flag);
+                  if (!go) break;
+                  const int tiles_q = n_tok > tpt ? 2 : 1;
+                  if (lane == 0) {
+                    const uint32_t bar = smem_u32(&sh.q_full);
+                    umma::mbar_expect_tx(bar, p.G * tpt * 128 * C::HALVES * tiles_q);
+                    for (int tt = 0; tt < tiles_q; ++tt)
+                      for (int half = 0; half < C::HALVES; ++half)
+                        umma::tma_load_3d(q_smem + tt * C::TILE + half * C::BOX, &q_map, half * 64,
+                                          h * p.G, un.tok0 + first + tt * tpt, bar);
+                  }
+                  ++n_item;
+                }
               }
             }
           }
-        }
-        // the next item
-        pos += cost;
-        if (++t == items) {
-          t = 0;
-          if (++h == p.Hkv) {
-            h = 0;
-            do {
-              if (++u == tile_units) break;
-              un = load_unit<SHARED>(p, u);
-              items = unit_items(un, tpt);
-            } while (items == 0);
-            if (u == tile_units) break;
+          // the next item
+          pos += cost;
+          if (++t == items) {
+            t = 0;
+            if (++h == p.Hkv) {
+              h = 0;
+              do {
+                if (++u == tile_units) break;
+                un = load_unit<SHARED>(p, u);
+                items = unit_items(un, tpt);
+              } while (items == 0);
+              if (u == tile_units) break;
+            }
           }
         }
       }
-    }
-    if (go) {
-      const int di = n_desc % kDescs;
-      go = wait(smem_u32(&sh.desc_empty[di]), ((n_desc / kDescs) & 1) ^ 1, abort_flag);
-      if (go && lane == 0) {
-        sh.desc[di].n_tok = 0;
-        umma::mbar_arrive(smem_u32(&sh.desc_full[di]));
+      if (go) {
+        const int di = n_desc % kDescs;
+        go = wait(smem_u32(&sh.desc_empty[di]), ((n_desc / kDescs) & 1) ^ 1, abort_flag);
+        if (go && lane == 0) {
+          sh.desc[di].n_tok = 0;
+          umma::mbar_arrive(smem_u32(&sh.desc_full[di]));
+        }
       }
-    }
-    if (!go) {  // copies in flight must land before the shared memory goes away
-      for (uint32_t i = 0; i < min(filled, (uint32_t)C::STAGES); ++i) {
-        const uint32_t use = filled - 1 - i;
+      if (!go) {  // copies in flight must land before the shared memory goes away
+        for (uint32_t i = 0; i < min(filled, (uint32_t)C::STAGES); ++i) {
+          const uint32_t use = filled - 1 - i;
+          const unsigned long long t0 = global_ns();
+          while (!umma::mbar_try_wait(smem_u32(&sh.kv_full[use % C::STAGES]),
+                                      (use / C::STAGES) & 1) &&
+                 global_ns() - t0 < kWaitNs) {
+          }
+        }
         const unsigned long long t0 = global_ns();
-        while (!umma::mbar_try_wait(smem_u32(&sh.kv_full[use % C::STAGES]),
-                                    (use / C::STAGES) & 1) &&
+        while (n_item > 0 && !umma::mbar_try_wait(smem_u32(&sh.q_full), (n_item - 1) & 1) &&
                global_ns() - t0 < kWaitNs) {
         }
       }
-      const unsigned long long t0 = global_ns();
-      while (n_item > 0 && !umma::mbar_try_wait(smem_u32(&sh.q_full), (n_item - 1) & 1) &&
-             global_ns() - t0 < kWaitNs) {
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    // ---- products ----------------------------------------------------------------------------
-    constexpr uint32_t kIdS = umma::idesc_bf16(kTile, kKeys, false, false);
-    constexpr uint32_t kIdO = umma::idesc_bf16(kTile, D, false, true);
-    int n_desc = 0, n_item = 0, n_tile = 0;
-    uint32_t p_phase[2] = {0, 0};
-    bool go = true;
-    auto scores = [&](int t, int st) {
+    } else if (warp == kMmaWarp) {
+      // ---- products ----------------------------------------------------------------------------
+      constexpr uint32_t kIdS = umma::idesc_bf16(kTile, kKeys, false, false);
+      constexpr uint32_t kIdO = umma::idesc_bf16(kTile, D, false, true);
+      int n_desc = 0, n_item = 0, n_tile = 0;
+      uint32_t p_phase[2] = {0, 0};
+      bool go = true;
+      auto scores = [&](int t, int st) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k / 4) * C::BOX + (k % 4) * 32;
-        umma::mma_bf16(tm + t * kKeys,
-                       umma::sdesc_sw128(q_smem + t * C::TILE + off, 0, 1024),
-                       umma::sdesc_sw128(kv_smem + st * C::TILE + off, 0, 1024), kIdS, k > 0);
-      }
-      umma::commit(smem_u32(&sh.s_full[t]));
-    };
-    auto values = [&](int t, int st, int half, bool more) {
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * C::BOX + (k % 4) * 32;
+          umma::mma_bf16(tm + t * kKeys,
+                         umma::sdesc_sw128(q_smem + t * C::TILE + off, 0, 1024),
+                         umma::sdesc_sw128(kv_smem + st * C::TILE + off, 0, 1024), kIdS, k > 0);
+        }
+        umma::commit(smem_u32(&sh.s_full[t]));
+      };
+      auto values = [&](int t, int st, int half, bool more) {
 #pragma unroll
-      for (int k = half * (kKeys / 32); k < (half + 1) * (kKeys / 32); ++k)
-        umma::mma_bf16_ta(tm + 2 * kKeys + t * D, tm + t * kKeys + k * 8,
-                          umma::sdesc_sw128(kv_smem + st * C::TILE + k * 2048, C::BOX, 1024), kIdO,
-                          more || k > 0);
-    };
-    while (true) {
-      const int di = n_desc % kDescs;
-      go = wait(smem_u32(&sh.desc_full[di]), (n_desc / kDescs) & 1, abort_flag);
-      if (!go) break;
-      const int n_tok = sh.desc[di].n_tok, j0 = sh.desc[di].j0, j1 = sh.desc[di].j1;
-      __syncwarp();
-      if (lane == 0) umma::mbar_arrive(smem_u32(&sh.desc_empty[di]));
-      ++n_desc;
-      if (n_tok == 0) break;
-      if (j0 == j1) continue;
-      const int nt = n_tok > tpt ? 2 : 1;
-      for (int j = j0; go && j <= j1; ++j) {
-        // step j: the values of tile j - 1, then the scores of tile j, row tile by row tile
-        const int kst = 2 * n_tile % C::STAGES, vst = (2 * n_tile - 1) % C::STAGES;
-        if (j == j0) go = wait(smem_u32(&sh.q_full), n_item & 1, abort_flag);
-        if (go && j < j1)
-          go = wait(smem_u32(&sh.kv_full[kst]), (2 * n_tile / C::STAGES) & 1, abort_flag);
-        if (go && j > j0)
-          go = wait(smem_u32(&sh.kv_full[vst]), ((2 * n_tile - 1) / C::STAGES) & 1, abort_flag);
-        for (int t = 0; go && t < nt; ++t) {
-          if (j > j0) {
-            go = wait(smem_u32(&sh.p_ready[t][0]), p_phase[t], abort_flag);
-            if (!go) break;
-            umma::fence_after_sync();
-            values(t, vst, 0, j > j0 + 1);
-            umma::commit(smem_u32(&sh.a_done[t]));
-            go = wait(smem_u32(&sh.p_ready[t][1]), p_phase[t], abort_flag);
-            if (!go) break;
-            umma::fence_after_sync();
-            values(t, vst, 1, true);
-            p_phase[t] ^= 1;
-            if (j == j1) umma::commit(smem_u32(&sh.o_full[t]));
-          } else {
-            umma::fence_after_sync();
+        for (int k = half * (kKeys / 32); k < (half + 1) * (kKeys / 32); ++k)
+          umma::mma_bf16_ta(tm + 2 * kKeys + t * D, tm + t * kKeys + k * 8,
+                            umma::sdesc_sw128(kv_smem + st * C::TILE + k * 2048, C::BOX, 1024),
+                            kIdO,
+                            more || k > 0);
+      };
+      while (true) {
+        const int di = n_desc % kDescs;
+        go = wait(smem_u32(&sh.desc_full[di]), (n_desc / kDescs) & 1, abort_flag);
+        if (!go) break;
+        const int n_tok = sh.desc[di].n_tok, j0 = sh.desc[di].j0, j1 = sh.desc[di].j1;
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(smem_u32(&sh.desc_empty[di]));
+        ++n_desc;
+        if (n_tok == 0) break;
+        if (j0 == j1) continue;
+        const int nt = n_tok > tpt ? 2 : 1;
+        for (int j = j0; go && j <= j1; ++j) {
+          // step j: the values of tile j - 1, then the scores of tile j, row tile by row tile
+          const int kst = 2 * n_tile % C::STAGES, vst = (2 * n_tile - 1) % C::STAGES;
+          if (j == j0) go = wait(smem_u32(&sh.q_full), n_item & 1, abort_flag);
+          if (go && j < j1)
+            go = wait(smem_u32(&sh.kv_full[kst]), (2 * n_tile / C::STAGES) & 1, abort_flag);
+          if (go && j > j0)
+            go = wait(smem_u32(&sh.kv_full[vst]), ((2 * n_tile - 1) / C::STAGES) & 1, abort_flag);
+          for (int t = 0; go && t < nt; ++t) {
+            if (j > j0) {
+              go = wait(smem_u32(&sh.p_ready[t][0]), p_phase[t], abort_flag);
+              if (!go) break;
+              umma::fence_after_sync();
+              values(t, vst, 0, j > j0 + 1);
+              umma::commit(smem_u32(&sh.a_done[t]));
+              go = wait(smem_u32(&sh.p_ready[t][1]), p_phase[t], abort_flag);
+              if (!go) break;
+              umma::fence_after_sync();
+              values(t, vst, 1, true);
+              p_phase[t] ^= 1;
+              if (j == j1) umma::commit(smem_u32(&sh.o_full[t]));
+            } else {
+              umma::fence_after_sync();
+            }
+            if (j < j1) scores(t, kst);
           }
-          if (j < j1) scores(t, kst);
+          if (!go) break;
+          if (j > j0) umma::commit(smem_u32(&sh.kv_empty[vst]));
+          if (j < j1) {
+            umma::commit(smem_u32(&sh.kv_empty[kst]));
+            if (j == j1 - 1) umma::commit(smem_u32(&sh.q_empty));
+            ++n_tile;
+          }
         }
         if (!go) break;
-        if (j > j0) umma::commit(smem_u32(&sh.kv_empty[vst]));
-        if (j < j1) {
-          umma::commit(smem_u32(&sh.kv_empty[kst]));
-          if (j == j1 - 1) umma::commit(smem_u32(&sh.q_empty));
-          ++n_tile;
+        ++n_item;
+      }
+      if (!go) {  // let what was issued finish
+        umma::commit(smem_u32(&sh.drain));
+        const unsigned long long t0 = global_ns();
+        while (!umma::mbar_try_wait(smem_u32(&sh.drain), 0) && global_ns() - t0 < kWaitNs) {
         }
       }
-      if (!go) break;
-      ++n_item;
     }
-    if (!go) {  // let what was issued finish
-      umma::commit(smem_u32(&sh.drain));
-      const unsigned long long t0 = global_ns();
-      while (!umma::mbar_try_wait(smem_u32(&sh.drain), 0) && global_ns() - t0 < kWaitNs) {
-      }
-    }
-  }
   } else {
     regs_more<kRegsSoftmax>();
     // ---- softmax and results -----------------------------------------------------------------
@@ -1358,7 +1362,8 @@ cudaError_t launch(const AttendParams& p, const Work& w, int ctas, cudaStream_t 
   const int64_t qd[3] = {D, (int64_t)p.Hkv * p.G, p.T}, qs[2] = {D, p.sq_t};
   const int qb[3] = {64, p.G, tpt};
   const int64_t kd[4] = {D, kPage, p.Hkv, p.kv.num_pages};
-  const int64_t ks[3] = {p.kv.sk_t, p.kv.sk_h, p.kv.sk_p}, vs[3] = {p.kv.sv_t, p.kv.sv_h, p.kv.sv_p};
+  const int64_t ks[3] = {p.kv.sk_t, p.kv.sk_h, p.kv.sk_p};
+  const int64_t vs[3] = {p.kv.sv_t, p.kv.sv_h, p.kv.sv_p};
   const int kb[4] = {64, kPage, 1, 1};
   if (!encode_fn() || !encode(&q, p.q, 3, qd, qs, qb) ||
       !encode(&k, p.kv.k_pool, 4, kd, ks, kb) || !encode(&v, p.kv.v_pool, 4, kd, vs, kb))
