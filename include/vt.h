@@ -315,9 +315,12 @@ vt_status vt_plan_requests(const int32_t* seq_lens, int32_t batch, int32_t* orde
  *   q_start     int32 [B+1], 0 = q_start[0] <= q_start[1] <= ... <= q_start[B] <= T; otherwise
  *               nothing is computed and VT_DEV_BAD_START is reported
  *   page_table, pt_stride, seq_lens, status   as in vt_decode_args
+ *   max_pages   entries of a page-table row that are the request's, 1 <= max_pages <= pt_stride
+ *               (a table that is some columns of a wider one has fewer than pt_stride); 0 means
+ *               pt_stride
  *   sm_scale    > 0
  * A request with no query tokens is skipped.  One with seq_lens[b] below its number of query
- * tokens, or of more pages than pt_stride, gets zero rows with lse = -inf (VT_DEV_BAD_LEN).  A
+ * tokens, or of more pages than max_pages, gets zero rows with lse = -inf (VT_DEV_BAD_LEN).  A
  * page id outside [0, num_pages) takes no part (VT_DEV_BAD_PAGE): the rows are the attention
  * over the request's other pages, zero with lse = -inf where none is left.  Pool slots behind
  * a request's last token are never used, whatever they hold; K and V of the tokens a request
@@ -339,6 +342,7 @@ typedef struct {
   const int32_t* seq_lens;
   float sm_scale;
   int32_t* status;
+  int64_t max_pages; /* 0: pt_stride */
 } vt_prefill_args;
 
 /*
@@ -366,11 +370,13 @@ size_t vt_prefill_workspace_size(const vt_paged_kv* kv, const vt_prefill_args* a
  *   group_start   int32 [num_groups+1], 0 = group_start[0] <= ... <= group_start[num_groups]
  *                 <= B; otherwise nothing is computed (VT_DEV_BAD_START).  Rows of requests at
  *                 or behind group_start[num_groups] are left as they were
- *   prefix_pages  int32 [num_groups], whole pages, 0 <= prefix_pages[g] <= pt_stride (outside:
+ *   prefix_pages  int32 [num_groups], whole pages, 0 <= prefix_pages[g] <= max_pages (outside:
  *                 VT_DEV_BAD_LEN and zero rows for the group); the entries are read from the
  *                 row of the group's first request
  *   seq_lens      all tokens of the request, the prefix among them, at least one and at least
- *                 16 prefix_pages[g] (otherwise VT_DEV_BAD_LEN and zero rows, lse = -inf)
+ *                 16 prefix_pages[g] (otherwise, or of more pages than max_pages,
+ *                 VT_DEV_BAD_LEN and zero rows, lse = -inf)
+ *   max_pages     as for vt_prefill
  * Bad page ids, unused slots, precision, head shapes and strides as for vt_prefill.
  */
 typedef struct {
@@ -385,6 +391,7 @@ typedef struct {
   const int32_t* seq_lens;
   float sm_scale;
   int32_t* status;
+  int64_t max_pages; /* 0: pt_stride */
 } vt_shared_prefix_args;
 
 /* out: bf16 [B, Hq, Dv]; lse: fp32 [B, Hq] or NULL; workspace as for vt_prefill. */
@@ -398,9 +405,10 @@ size_t vt_shared_prefix_workspace_size(const vt_paged_kv* kv, const vt_shared_pr
 /*
  * ---- pages of the cache ------------------------------------------------------------------
  *
- * The cache's books are three int32 device arrays of the caller: page_table [R, pt_stride],
- * seq_lens [R] (0: the row holds no request) and refs [num_pages], the number of rows that
- * use a page (0: free).  The calls below change the books, and the pools where pages are
+ * The cache's books are three int32 device arrays of the caller: page_table, R rows of max_pages
+ * entries that stand pt_stride apart (1 <= max_pages <= pt_stride, 0 means pt_stride; what is
+ * between the rows is neither read nor written), seq_lens [R] (0: the row holds no request) and
+ * refs [num_pages], the number of rows that use a page (0: free).  The calls below change the books, and the pools where pages are
  * copied, on the device; nothing is read back.  Pages are always taken lowest free id first,
  * in the order of the list, so results do not depend on timing.  Calls on the same books must
  * be ordered (one stream, or events).  Lists are int32 device arrays; entries outside [0, R)
@@ -415,6 +423,7 @@ typedef struct {
   int32_t* seq_lens;
   int32_t* refs;
   int32_t* status;
+  int64_t max_pages; /* 0: pt_stride */
 } vt_page_books;
 
 /*
@@ -430,7 +439,7 @@ vt_status vt_copy_pages(const vt_paged_kv* kv, const int32_t* src, const int32_t
  * its full pages (refs + 1); a partly filled last page is copied to a page of its own, so that
  * both can grow.  A parent may be listed often; a child must hold no request (seq_lens 0) and
  * be listed once: other entries, and an empty parent's, are left out with VT_DEV_BAD_REQ (a
- * child listed twice takes its first entry), a parent of more pages than pt_stride with
+ * child listed twice takes its first entry), a parent of more pages than max_pages with
  * VT_DEV_BAD_LEN.  A bad page id in a parent's row goes into the child's as it is, or leaves
  * the copy's contents open (VT_DEV_BAD_PAGE).  With f free pages, the entries that need a page
  * get one while the count of such entries up to and including them is at most f; the others
@@ -445,7 +454,7 @@ vt_status vt_fork_requests(const vt_paged_kv* kv, const vt_page_books* books,
 /*
  * Row requests[i] grows by tokens[i] >= 0 tokens (a new request from length 0), i < n; the pages
  * that this takes are appended to its row, with one reference.  A growth that is negative or
- * past 16 pt_stride tokens is left out (VT_DEV_BAD_LEN); a row listed twice grows by its first
+ * past 16 max_pages tokens is left out (VT_DEV_BAD_LEN); a row listed twice grows by its first
  * entry (VT_DEV_BAD_REQ).  With f free pages, an entry gets its pages if the pages that the
  * entries up to and including it need are at most f; otherwise it is left as it was
  * (VT_DEV_NO_PAGE).  An entry that needs no page is always served.  workspace: as for
@@ -459,7 +468,7 @@ vt_status vt_extend_requests(const vt_page_books* books, int64_t num_pages,
  * Rows requests[i] end, i < n: every page of the row loses a reference, seq_lens becomes 0; the
  * table entries stay as they are.  A row listed twice, or empty, is freed once, or not.  A bad
  * page id is skipped (VT_DEV_BAD_PAGE), a page without a reference keeps 0 (VT_DEV_BAD_REF); a
- * row of more pages than pt_stride frees those of its entries (VT_DEV_BAD_LEN).
+ * row of more pages than max_pages frees those of its entries (VT_DEV_BAD_LEN).
  */
 vt_status vt_free_requests(const vt_page_books* books, int64_t num_pages, const int32_t* requests,
                            int32_t n, void* stream);

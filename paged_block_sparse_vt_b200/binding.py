@@ -57,7 +57,7 @@ class PrefillArgs(ctypes.Structure):
         ("num_tokens", ctypes.c_int64), ("q", ctypes.c_void_p), ("sq_t", ctypes.c_int64),
         ("q_start", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
         ("pt_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p),
-        ("sm_scale", ctypes.c_float), ("status", ctypes.c_void_p),
+        ("sm_scale", ctypes.c_float), ("status", ctypes.c_void_p), ("max_pages", ctypes.c_int64),
     ]
 
 
@@ -68,7 +68,7 @@ class SharedPrefixArgs(ctypes.Structure):
         ("group_start", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p),
         ("page_table", ctypes.c_void_p), ("pt_stride", ctypes.c_int64),
         ("seq_lens", ctypes.c_void_p), ("sm_scale", ctypes.c_float),
-        ("status", ctypes.c_void_p),
+        ("status", ctypes.c_void_p), ("max_pages", ctypes.c_int64),
     ]
 
 
@@ -76,6 +76,7 @@ class PageBooks(ctypes.Structure):
     _fields_ = [
         ("rows", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("pt_stride", ctypes.c_int64),
         ("seq_lens", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("status", ctypes.c_void_p),
+        ("max_pages", ctypes.c_int64),
     ]
 
 
@@ -458,7 +459,8 @@ def _sized(t: torch.Tensor, name: str, shape: tuple) -> None:
 
 
 def _table(page_table: torch.Tensor, dev: int):
-    """(rows, row stride) of a page table."""
+    """(rows, row stride, entries of a row) of a page table; what is between the rows of a view of
+    some columns is not the table's."""
     if not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32 \
             or page_table.get_device() != dev:
         _fail(page_table, "page_table", torch.int32, dev, contiguous=False)
@@ -466,7 +468,8 @@ def _table(page_table: torch.Tensor, dev: int):
     if len(st) != 2 or st[1] != 1:
         raise VtError(VT_ERR_INVALID_ARG, "page_table", "must be [B, max_pages] with unit inner stride")
     rows, width = page_table.shape
-    return rows, st[0] if rows > 1 else width
+    stride = st[0] if rows > 1 else width
+    return rows, stride, min(width, stride)
 
 
 def _pools(k_pool, v_pool, dev: int) -> PagedKV:
@@ -506,7 +509,7 @@ def _gpu(t, name: str) -> int:
 def _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, status):
     dev = _gpu(q, "q")
     kv = _pools(k_pool, v_pool, dev)
-    B, pt_stride = _table(page_table, dev)
+    B, pt_stride, max_pages = _table(page_table, dev)
     if q.dtype is not torch.bfloat16:
         _need(q, "q", torch.bfloat16)
     if q.dim() != 3 or q.shape[2] != kv.head_dim:
@@ -521,7 +524,7 @@ def _prefill_args(q, k_pool, v_pool, page_table, seq_lens, q_start, sm_scale, st
     _sized(q_start, "q_start", (B + 1,))
     return kv, PrefillArgs(B, hq, T, q.data_ptr(), st if T > 1 else hq * d, start,
                            page_table.data_ptr(), pt_stride, seq, float(sm_scale),
-                           _status(status, dev))
+                           _status(status, dev), max_pages)
 
 
 def _attend_outputs(q, out, lse, want_lse):
@@ -619,7 +622,7 @@ def _shared_args(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pa
                  status):
     dev = _gpu(q, "q")
     kv = _pools(k_pool, v_pool, dev)
-    B, pt_stride = _table(page_table, dev)
+    B, pt_stride, max_pages = _table(page_table, dev)
     qp = _vec(q, "q", torch.bfloat16, dev)
     if q.dim() != 3 or q.shape[0] != B or q.shape[2] != kv.head_dim:
         raise VtError(VT_ERR_INVALID_ARG, "q", f"must be [{B}, Hq, {kv.head_dim}]")
@@ -631,7 +634,7 @@ def _shared_args(q, k_pool, v_pool, page_table, seq_lens, group_start, prefix_pa
     _sized(group_start, "group_start", (groups + 1,))
     _sized(prefix_pages, "prefix_pages", (groups,))
     return kv, SharedPrefixArgs(B, q.shape[1], groups, qp, start, prefix, page_table.data_ptr(),
-                                pt_stride, seq, float(sm_scale), _status(status, dev))
+                                pt_stride, seq, float(sm_scale), _status(status, dev), max_pages)
 
 
 def _shared_ws(lib, dev: int, kv: PagedKV, a: SharedPrefixArgs) -> int:
@@ -671,11 +674,11 @@ def vt_shared_prefix_decode(q, k_pool, v_pool, page_table, seq_lens, group_start
 
 
 def _books(page_table, seq_lens, refs, status, dev: int) -> PageBooks:
-    rows, pt_stride = _table(page_table, dev)
+    rows, pt_stride, max_pages = _table(page_table, dev)
     seq = _vec(seq_lens, "seq_lens", torch.int32, dev)
     _sized(seq_lens, "seq_lens", (rows,))
     return PageBooks(rows, page_table.data_ptr(), pt_stride, seq,
-                     _vec(refs, "refs", torch.int32, dev), _status(status, dev))
+                     _vec(refs, "refs", torch.int32, dev), _status(status, dev), max_pages)
 
 
 def _lists(dev: int, first, second, names: tuple):

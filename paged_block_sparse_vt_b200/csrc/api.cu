@@ -295,9 +295,21 @@ vt_status check_workspace(const void* ws, size_t ws_bytes, size_t need) {
   return ok();
 }
 
+// A page table's row stride, and the entries of a row (`max_pages`, 0 for all of the stride).
+vt_status check_table(int64_t pt_stride, int64_t max_pages, int64_t* entries) {
+  if (pt_stride < 1 || pt_stride > VT_MAX_PAGES_PER_REQUEST)
+    return fail(VT_ERR_UNSUPPORTED, "pt_stride %lld outside [1, %d]", (long long)pt_stride,
+                VT_MAX_PAGES_PER_REQUEST);
+  if (max_pages < 0 || max_pages > pt_stride)
+    return fail(VT_ERR_INVALID_ARG, "max_pages %lld outside [0, pt_stride %lld]",
+                (long long)max_pages, (long long)pt_stride);
+  *entries = max_pages ? max_pages : pt_stride;
+  return ok();
+}
+
 // What both dense attention calls ask of the pools, the heads and the page table.
 vt_status attend_common(const vt_paged_kv* kv, int batch, int Hq, const void* q, int64_t pt_stride,
-                        float sm_scale, AttendParams* p) {
+                        int64_t max_pages, float sm_scale, AttendParams* p) {
   Shape sh;
   vt_status s = classify(kv, Hq, &sh);
   if (s != VT_OK) return s;
@@ -314,9 +326,9 @@ vt_status attend_common(const vt_paged_kv* kv, int batch, int Hq, const void* q,
   if (batch < 0) return fail(VT_ERR_INVALID_ARG, "batch < 0");
   if (batch > 65536) return fail(VT_ERR_UNSUPPORTED, "batch > 65536");
   if (Hq > 32767) return fail(VT_ERR_UNSUPPORTED, "num_q_heads > 32767");
-  if (pt_stride < 1 || pt_stride > VT_MAX_PAGES_PER_REQUEST)
-    return fail(VT_ERR_UNSUPPORTED, "pt_stride %lld outside [1, %d]", (long long)pt_stride,
-                VT_MAX_PAGES_PER_REQUEST);
+  int64_t entries;
+  s = check_table(pt_stride, max_pages, &entries);
+  if (s != VT_OK) return s;
   if (!std::isfinite(sm_scale * kLog2e) || !(sm_scale > 0.0f))
     return fail(VT_ERR_INVALID_ARG, "sm_scale must be positive and finite");
   if (!aligned16(q)) return fail(VT_ERR_UNSUPPORTED, "q not 16-byte aligned");
@@ -328,6 +340,7 @@ vt_status attend_common(const vt_paged_kv* kv, int batch, int Hq, const void* q,
   p->B = batch;
   p->q = static_cast<const __nv_bfloat16*>(q);
   p->pt_stride = pt_stride;
+  p->max_pages = entries;
   p->qscale = sm_scale * kLog2e;
   return ok();
 }
@@ -336,7 +349,8 @@ vt_status prefill_params(const vt_paged_kv* kv, const vt_prefill_args* a, Attend
   vt_status s = check_kv(kv);
   if (s != VT_OK) return s;
   if (!a) return fail(VT_ERR_INVALID_ARG, "args is NULL");
-  s = attend_common(kv, a->batch, a->num_q_heads, a->q, a->pt_stride, a->sm_scale, p);
+  s = attend_common(kv, a->batch, a->num_q_heads, a->q, a->pt_stride, a->max_pages, a->sm_scale,
+                    p);
   if (s != VT_OK) return s;
   if (a->num_tokens < 0) return fail(VT_ERR_INVALID_ARG, "num_tokens < 0");
   if (a->num_tokens > ((int64_t)1 << 30)) return fail(VT_ERR_UNSUPPORTED, "num_tokens > 2^30");
@@ -361,7 +375,8 @@ vt_status shared_params(const vt_paged_kv* kv, const vt_shared_prefix_args* a, A
   vt_status s = check_kv(kv);
   if (s != VT_OK) return s;
   if (!a) return fail(VT_ERR_INVALID_ARG, "args is NULL");
-  s = attend_common(kv, a->batch, a->num_q_heads, a->q, a->pt_stride, a->sm_scale, p);
+  s = attend_common(kv, a->batch, a->num_q_heads, a->q, a->pt_stride, a->max_pages, a->sm_scale,
+                    p);
   if (s != VT_OK) return s;
   if (a->num_groups < 0) return fail(VT_ERR_INVALID_ARG, "num_groups < 0");
   if (a->num_groups > 65536) return fail(VT_ERR_UNSUPPORTED, "num_groups > 65536");
@@ -412,14 +427,13 @@ PageWorkspace page_workspace(int64_t num_pages, int32_t n) {
   return w;
 }
 
-vt_status check_books(const vt_page_books* b, int64_t num_pages) {
+vt_status check_books(const vt_page_books* b, int64_t num_pages, int64_t* entries) {
   if (!b) return fail(VT_ERR_INVALID_ARG, "books is NULL");
   if (num_pages < 1) return fail(VT_ERR_INVALID_ARG, "num_pages < 1");
   if (num_pages > (int64_t)INT32_MAX) return fail(VT_ERR_UNSUPPORTED, "num_pages above 2^31-1");
   if (b->rows < 0) return fail(VT_ERR_INVALID_ARG, "rows < 0");
-  if (b->pt_stride < 1 || b->pt_stride > VT_MAX_PAGES_PER_REQUEST)
-    return fail(VT_ERR_UNSUPPORTED, "pt_stride %lld outside [1, %d]", (long long)b->pt_stride,
-                VT_MAX_PAGES_PER_REQUEST);
+  vt_status s = check_table(b->pt_stride, b->max_pages, entries);
+  if (s != VT_OK) return s;
   if (!b->refs || (b->rows > 0 && (!b->page_table || !b->seq_lens)))
     return fail(VT_ERR_INVALID_ARG, "page_table/seq_lens/refs is NULL");
   return ok();
@@ -446,12 +460,13 @@ vt_status page_pools(const vt_paged_kv* kv, float* centroids, PagePools* p, int*
   return ok();
 }
 
-PageListParams list_params(const vt_page_books* b, int64_t num_pages, const int32_t* sources,
-                           const int32_t* targets, int32_t n, void* ws) {
+PageListParams list_params(const vt_page_books* b, int64_t entries, int64_t num_pages,
+                           const int32_t* sources, const int32_t* targets, int32_t n, void* ws) {
   PageListParams p{};
   p.rows = b->rows;
   p.page_table = b->page_table;
   p.pt_stride = b->pt_stride;
+  p.max_pages = entries;
   p.seq_lens = b->seq_lens;
   p.refs = b->refs;
   p.status = b->status;
@@ -674,14 +689,16 @@ vt_status vt_fork_requests(const vt_paged_kv* kv, const vt_page_books* books,
   int sides;
   vt_status s = page_pools(kv, nullptr, &pools, &sides);
   if (s != VT_OK) return s;
-  s = check_books(books, kv->num_pages);
+  int64_t entries;
+  s = check_books(books, kv->num_pages, &entries);
   if (s != VT_OK) return s;
   if (n < 0) return fail(VT_ERR_INVALID_ARG, "n < 0");
   if (n == 0) return ok();
   if (!parents || !children) return fail(VT_ERR_INVALID_ARG, "parents/children is NULL");
   s = check_workspace(workspace, workspace_bytes, page_workspace(kv->num_pages, n).total);
   if (s != VT_OK) return s;
-  const PageListParams p = list_params(books, kv->num_pages, parents, children, n, workspace);
+  const PageListParams p =
+      list_params(books, entries, kv->num_pages, parents, children, n, workspace);
   cudaError_t e = launch_fork(pools, p, sides, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fork_requests launch");
   return ok();
@@ -690,7 +707,8 @@ vt_status vt_fork_requests(const vt_paged_kv* kv, const vt_page_books* books,
 vt_status vt_extend_requests(const vt_page_books* books, int64_t num_pages,
                              const int32_t* requests, const int32_t* tokens, int32_t n,
                              void* workspace, size_t workspace_bytes, void* stream) {
-  vt_status s = check_books(books, num_pages);
+  int64_t entries;
+  vt_status s = check_books(books, num_pages, &entries);
   if (s != VT_OK) return s;
   if (n < 0) return fail(VT_ERR_INVALID_ARG, "n < 0");
   if (n == 0) return ok();
@@ -699,7 +717,8 @@ vt_status vt_extend_requests(const vt_page_books* books, int64_t num_pages,
     s = check_workspace(workspace, workspace_bytes, page_workspace(num_pages, n).total);
     if (s != VT_OK) return s;
   }
-  const PageListParams p = list_params(books, num_pages, tokens, requests, n, workspace);
+  const PageListParams p =
+      list_params(books, entries, num_pages, tokens, requests, n, workspace);
   cudaError_t e = launch_extend(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "extend_requests launch");
   return ok();
@@ -707,12 +726,14 @@ vt_status vt_extend_requests(const vt_page_books* books, int64_t num_pages,
 
 vt_status vt_free_requests(const vt_page_books* books, int64_t num_pages, const int32_t* requests,
                            int32_t n, void* stream) {
-  vt_status s = check_books(books, num_pages);
+  int64_t entries;
+  vt_status s = check_books(books, num_pages, &entries);
   if (s != VT_OK) return s;
   if (n < 0) return fail(VT_ERR_INVALID_ARG, "n < 0");
   if (n == 0) return ok();
   if (!requests) return fail(VT_ERR_INVALID_ARG, "requests is NULL");
-  cudaError_t e = launch_free(*books, num_pages, requests, n, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_free(*books, entries, num_pages, requests, n,
+                              static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "free_requests launch");
   return ok();
 }
@@ -724,7 +745,8 @@ vt_status vt_compact_pages(const vt_paged_kv* kv, const vt_page_books* books, fl
   int sides;
   vt_status s = page_pools(kv, centroids, &pools, &sides);
   if (s != VT_OK) return s;
-  s = check_books(books, kv->num_pages);
+  int64_t entries;
+  s = check_books(books, kv->num_pages, &entries);
   if (s != VT_OK) return s;
   if (!n_used) return fail(VT_ERR_INVALID_ARG, "n_used is NULL");
   const PageWorkspace w = page_workspace(kv->num_pages, 0);
@@ -734,6 +756,7 @@ vt_status vt_compact_pages(const vt_paged_kv* kv, const vt_page_books* books, fl
   p.rows = books->rows;
   p.page_table = books->page_table;
   p.pt_stride = books->pt_stride;
+  p.max_pages = entries;
   p.seq_lens = books->seq_lens;
   p.refs = books->refs;
   p.status = books->status;

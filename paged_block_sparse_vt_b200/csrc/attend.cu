@@ -137,7 +137,7 @@ __device__ __forceinline__ int group_of(const AttendParams& p, int b) {
 // Pages that a group shares as far as this call goes (a group of one shares with nobody); -1 bad.
 __device__ __forceinline__ int group_prefix(const AttendParams& p, int g) {
   const int pages = p.prefix_pages[g];
-  if (pages < 0 || pages > p.pt_stride) return -1;
+  if (pages < 0 || pages > p.max_pages) return -1;
   return p.start[g + 1] - p.start[g] >= 2 ? pages : 0;
 }
 
@@ -150,7 +150,7 @@ __device__ Unit load_unit(const AttendParams& p, int u) {
     x.n = p.start[u + 1] - x.tok0;
     x.row = u;
     if (x.n == 0) return x;  // whatever its length
-    x.bad = len < x.n || len > p.pt_stride * kPage;
+    x.bad = len < x.n || len > p.max_pages * kPage;
     x.kv_len = x.bad ? 0 : len;
     x.vis0 = x.bad ? 0 : len - x.n + 1;
     x.step = x.bad ? 0 : 1;
@@ -165,7 +165,7 @@ __device__ Unit load_unit(const AttendParams& p, int u) {
     if (g < 0) return x;
     x.n = 1;
     const int len = p.seq_lens[b], pages = group_prefix(p, g);
-    x.bad = pages < 0 || len < 1 || len > p.pt_stride * kPage ||
+    x.bad = pages < 0 || len < 1 || len > p.max_pages * kPage ||
             len < p.prefix_pages[g] * kPage;
     x.page0 = max(pages, 0);
     x.kv_len = x.vis0 = x.bad ? 0 : len - x.page0 * kPage;
@@ -1292,7 +1292,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // not, no item is cut, and there is nothing to join and no workspace.
 bool may_split(const AttendParams& p) {
   const int64_t tpt = kTile / p.G, items = p.Hkv * (p.T / (2 * tpt) + std::min<int64_t>(p.B, p.T));
-  return items * kCostTwo * (kCostItem + p.pt_stride * kPage) >= 2 * kMinShare;
+  return items * kCostTwo * (kCostItem + p.max_pages * kPage) >= 2 * kMinShare;
 }
 
 // Fills w from ws (NULL: only the size is wanted) and returns the bytes.

@@ -22,6 +22,7 @@ struct AttendParams {
   const int32_t* prefix_pages;  // [n_groups]; prompts: NULL
   const int32_t* page_table;
   int64_t pt_stride;
+  int64_t max_pages;  // entries of a table row
   const int32_t* seq_lens;
   float qscale;      // sm_scale log2(e)
   int32_t* status;

@@ -1,8 +1,8 @@
 // pages.cu -- the pages of the cache on the device: copying, forking, growing, ending and
 // compacting requests over a pool of reference-counted pages.
 //
-// The books are page_table [R, pt_stride], seq_lens [R] and refs [P].  A page is free where its
-// count is 0, and the k-th page that a call takes is the free page of rank k,
+// The books are page_table [R, max_pages] (rows pt_stride apart), seq_lens [R] and refs [P].  A
+// page is free where its count is 0, and the k-th page that a call takes is the free page of rank k,
 //   rank(x) = #{y < x : refs[y] == 0},
 // so what a call does follows from the books alone: the only atomics are sums and minima of
 // integers, whose order does not show.
@@ -122,13 +122,13 @@ __device__ int read_list(const PageListParams& p, const Lists& a, int* s_warp) {
       } else {
         len = p.seq_lens[source];
         if (len <= 0) bad = VT_DEV_BAD_REQ;
-        else if (pages_of(len) > p.pt_stride) bad = VT_DEV_BAD_LEN;
+        else if (pages_of(len) > p.max_pages) bad = VT_DEV_BAD_LEN;
         need = len % kPage != 0;
       }
     } else {
       len = p.seq_lens[row];
       const int64_t grown = (int64_t)len + source;
-      if (len < 0 || source < 0 || grown > p.pt_stride * kPage || grown > INT32_MAX)
+      if (len < 0 || source < 0 || grown > p.max_pages * kPage || grown > INT32_MAX)
         bad = VT_DEV_BAD_LEN;
       else
         need = pages_of((int)grown) - pages_of(len);
@@ -336,8 +336,9 @@ __global__ void __launch_bounds__(kCopyThreads)
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
-    free_kernel(int rows, const int32_t* page_table, int64_t pt_stride, int32_t* seq_lens,
-                int32_t* refs, int64_t num_pages, const int32_t* requests, int32_t* status) {
+    free_kernel(int rows, const int32_t* page_table, int64_t pt_stride, int64_t max_pages,
+                int32_t* seq_lens, int32_t* refs, int64_t num_pages, const int32_t* requests,
+                int32_t* status) {
   __shared__ int s_len;
   const int row = requests[blockIdx.x];
   if (row < 0 || row >= rows) {
@@ -348,9 +349,9 @@ __global__ void __launch_bounds__(kCopyThreads)
   __syncthreads();
   if (s_len <= 0) return;
   int n = pages_of(s_len);
-  if (n > pt_stride) {
+  if (n > max_pages) {
     if (threadIdx.x == 0) flag(status, VT_DEV_BAD_LEN);
-    n = (int)pt_stride;
+    n = (int)max_pages;
   }
   for (int k = threadIdx.x; k < n; k += kCopyThreads) {
     const int page = page_table[(int64_t)row * pt_stride + k];
@@ -437,9 +438,9 @@ __global__ void __launch_bounds__(kCopyThreads)
     const int len = p.seq_lens[row];
     if (len <= 0) continue;
     int n = pages_of(len);
-    if (n > p.pt_stride) {
+    if (n > p.max_pages) {
       if (threadIdx.x == 0) flag(p.status, VT_DEV_BAD_LEN);
-      n = (int)p.pt_stride;
+      n = (int)p.max_pages;
     }
     int32_t* t = p.page_table + (int64_t)row * p.pt_stride;
     for (int k = threadIdx.x; k < n; k += kCopyThreads) {
@@ -478,10 +479,10 @@ cudaError_t launch_extend(const PageListParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_free(const vt_page_books& b, int64_t num_pages, const int32_t* requests, int n,
-                        cudaStream_t s) {
-  free_kernel<<<n, kCopyThreads, 0, s>>>(b.rows, b.page_table, b.pt_stride, b.seq_lens, b.refs,
-                                         num_pages, requests, b.status);
+cudaError_t launch_free(const vt_page_books& b, int64_t max_pages, int64_t num_pages,
+                        const int32_t* requests, int n, cudaStream_t s) {
+  free_kernel<<<n, kCopyThreads, 0, s>>>(b.rows, b.page_table, b.pt_stride, max_pages, b.seq_lens,
+                                         b.refs, num_pages, requests, b.status);
   return cudaGetLastError();
 }
 

@@ -30,6 +30,7 @@ struct PageListParams {
   int rows;
   int32_t* page_table;
   int64_t pt_stride;
+  int64_t max_pages;  // entries of a table row
   int32_t* seq_lens;
   int32_t* refs;
   int32_t* status;
@@ -47,6 +48,7 @@ struct CompactParams {
   int rows;
   int32_t* page_table;
   int64_t pt_stride;
+  int64_t max_pages;  // entries of a table row
   const int32_t* seq_lens;
   int32_t* refs;
   int32_t* status;
@@ -62,8 +64,8 @@ cudaError_t launch_copy_pages(const PagePools& pools, const int32_t* src, const 
                               int sides, int32_t* status, cudaStream_t s);
 cudaError_t launch_fork(const PagePools& pools, const PageListParams& p, int sides, cudaStream_t s);
 cudaError_t launch_extend(const PageListParams& p, cudaStream_t s);
-cudaError_t launch_free(const vt_page_books& b, int64_t num_pages, const int32_t* requests, int n,
-                        cudaStream_t s);
+cudaError_t launch_free(const vt_page_books& b, int64_t max_pages, int64_t num_pages,
+                        const int32_t* requests, int n, cudaStream_t s);
 cudaError_t launch_compact(const PagePools& pools, const CompactParams& p, int sides, int sm_count,
                            cudaStream_t s);
 
