@@ -117,6 +117,7 @@ struct Shared {
   int bad[kBadRing];
   uint64_t q_full, q_empty, s_full[2], p_ready[2][2], a_done[2], o_full[2], desc_full[kDescs],
       desc_empty[kDescs], kv_full[8], kv_empty[8], drain;
+  int64_t total[2];  // the lines' lengths (the tables themselves give way to q)
   uint32_t tmem;
   int abort;
 };
@@ -513,10 +514,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       before += c;
     }
     if (lane == 0) line[0] = 0;
+    if (lane == 31) sh.total[warp] = before;
   }
+  // Behind this barrier the loading warp may have q written over the tables at any time: of the
+  // other warps only those read them that a further barrier holds back.
   __syncthreads();
   if (!fine && cta == 0 && threadIdx.x == 0) flag(p.status, VT_DEV_BAD_START);
-  const int64_t total = fine ? table0[entries] : 0, pages = SHARED && fine ? table1[entries] : 0;
+  const int64_t total = fine ? sh.total[0] : 0, pages = SHARED && fine ? sh.total[1] : 0;
   const int split = SHARED ? first_own(total, pages, gridDim.x) : gridDim.x;
   const Line tiles_line = make_line(total, max(split, 1), kMinShare);
 

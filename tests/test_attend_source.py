@@ -1,0 +1,40 @@
+"""What csrc/attend.cu must keep to where a run would show it only by chance: read in the source.
+
+The kernel's cost tables lie where the loading warp later has q written by an asynchronous copy."""
+import os
+import re
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def source():
+    with open(os.path.join(ROOT, "paged_block_sparse_vt_b200", "csrc", "attend.cu")) as f:
+        text = f.read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def between(text, start, end):
+    i = text.index(start)
+    return text[i:text.index(end, i)]
+
+
+def test_no_warp_reads_the_cost_tables_while_q_may_come():
+    """Behind the barrier that ends their making, the tables are read by the loading warp itself,
+    and elsewhere only in blocks that end in a barrier, before any role begins."""
+    body = between(source(), "attend_kernel(const AttendParams p", "struct Join")
+    after = body[body.index("flag(p.status, VT_DEV_BAD_START)"):]
+    roles = after[:after.index("if (warp >= kLoadWarp)")]
+    reads = [m.start() for m in re.finditer(r"table[01]\b", roles)]
+    assert reads
+    for at in reads:
+        rest = roles[at:]
+        # the loading warp's own name for its line, used in its role only
+        if re.match(r"table0;", rest):
+            continue
+        assert "__syncthreads();" in rest, roles[max(0, at - 80):at + 40]
+    first = roles[:roles.index("if (SHARED && cta ==")]
+    assert not re.search(r"table[01]\b", first), first
+    # past the roles' start nobody but the loading warp follows that name
+    loading = between(after, "if (warp == kLoadWarp)", "else if (warp == kMmaWarp)")
+    uses = len(re.findall(r"\bline\[", after[after.index("if (warp >= kLoadWarp)"):]))
+    assert uses == len(re.findall(r"\bline\[", loading)) > 0
