@@ -176,13 +176,15 @@ __device__ Unit load_unit(const AttendParams& p, int u) {
 
 // ---- bounded waits --------------------------------------------------------------------------
 
+// Whole warp, and one answer for all of it: what follows are shuffles, votes and tensor-memory
+// instructions of the whole warp, so no lane may go on where another gives up.  Lanes that polled
+// each for itself could part: one sees the phase complete, another the flag that a third set.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase, volatile int* abort_flag) {
   for (int i = 0; i < 64; ++i)
-    if (umma::mbar_try_wait(bar, phase)) return true;
+    if (__all_sync(kFull, umma::mbar_try_wait(bar, phase))) return true;
   const unsigned long long t0 = global_ns();
-  while (!umma::mbar_try_wait(bar, phase)) {
-    if (*abort_flag) return false;
-    if (global_ns() - t0 > kWaitNs) {
+  while (!__all_sync(kFull, umma::mbar_try_wait(bar, phase))) {
+    if (__any_sync(kFull, *abort_flag != 0 || global_ns() - t0 > kWaitNs)) {
       *abort_flag = 1;
       return false;
     }

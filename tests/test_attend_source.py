@@ -38,3 +38,26 @@ def test_no_warp_reads_the_cost_tables_while_q_may_come():
     loading = between(after, "if (warp == kLoadWarp)", "else if (warp == kMmaWarp)")
     uses = len(re.findall(r"\bline\[", after[after.index("if (warp >= kLoadWarp)"):]))
     assert uses == len(re.findall(r"\bline\[", loading)) > 0
+
+
+def test_a_bounded_wait_has_one_answer_for_the_warp():
+    """The phase is polled, and given up, by vote; and whole warps call it."""
+    text = source()
+    body = between(text, "bool wait(uint32_t bar", "\n}\n")
+    polls = re.findall(r"(\S*\(\w*,? ?)?umma::mbar_try_wait", body)
+    assert polls and all(x == "(__all_sync(kFull, " or x.endswith("__all_sync(kFull, ")
+                         for x in polls), polls
+    gives_up = between(body, "while (", "return false")
+    assert re.search(r"if \(__any_sync\(kFull, \*abort_flag != 0 \|\| global_ns\(\) - t0 > kWaitNs\)\)",
+                     gives_up)
+    assert body.count("return false") == 1
+    # nothing that calls it stands in a lane's own block
+    for m in re.finditer(r"\bwait\(smem_u32", text):
+        line = text[text.rfind("\n", 0, m.start()) + 1:m.start()]
+        assert "lane" not in line, line
+    for block in re.finditer(r"if \(lane == 0[^{;]*\{", text):
+        depth, i = 1, block.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(text[i], 0)
+            i += 1
+        assert not re.search(r"\bwait\(", text[block.end():i])
