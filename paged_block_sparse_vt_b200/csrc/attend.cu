@@ -1004,9 +1004,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               hand_over(h);
             }
           }
-        } else if (lane == 0) {
-          umma::mbar_arrive(smem_u32(&sh.p_ready[t][0]));
-          umma::mbar_arrive(smem_u32(&sh.p_ready[t][1]));
+        } else {
+          // (no weights of its own, but it may just have read the last item's O, which the product
+          // behind this arrival overwrites)
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            umma::mbar_arrive(smem_u32(&sh.p_ready[t][0]));
+            umma::mbar_arrive(smem_u32(&sh.p_ready[t][1]));
+          }
         }
       }
       if (!ok) break;

@@ -61,3 +61,16 @@ def test_a_bounded_wait_has_one_answer_for_the_warp():
             depth += {"{": 1, "}": -1}.get(text[i], 0)
             i += 1
         assert not re.search(r"\bwait\(", text[block.end():i])
+
+
+def test_every_arrival_for_the_product_warp_stands_behind_the_tensor_memory_fence():
+    """A p_ready arrival lets O and S be overwritten: what its warp read from them is ordered first,
+    whether or not the warp has rows of its own in this item."""
+    text = source()
+    arrivals = [m.start() for m in re.finditer(r"mbar_arrive\(smem_u32\(&sh\.p_ready", text)]
+    assert len(arrivals) == 3
+    for at in arrivals:
+        before = text[:at]
+        # the last thing that is not an arrival, a lane's guard or a warp barrier
+        block = re.sub(r"(umma::mbar_arrive\([^;]*;|if \(lane == 0\) ?\{?|__syncwarp\(\);|\s)+$", "", before)
+        assert block.endswith("umma::fence_before_sync();"), block[-120:]
