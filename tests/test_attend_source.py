@@ -67,7 +67,7 @@ def test_every_arrival_for_the_product_warp_stands_behind_the_tensor_memory_fenc
     """A p_ready arrival lets O and S be overwritten: what its warp read from them is ordered first,
     whether or not the warp has rows of its own in this item."""
     text = source()
-    arrivals = [m.start() for m in re.finditer(r"mbar_arrive\(smem_u32\(&sh\.p_ready", text)]
+    arrivals = [m.start() for m in re.finditer(r"umma::mbar_arrive\(smem_u32\(&sh\.p_ready", text)]
     assert len(arrivals) == 3
     for at in arrivals:
         before = text[:at]
