@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.head[2 * cta + 1].valid = 0;
       }
       int n_desc = 0, n_item = 0, n_tile = 0;
-      uint32_t filled = 0;  // stage uses, for the drain behind an abort
+      uint32_t filled = 0;  // stage uses, for the drain
       bool go = true;
       if (work) {
         const int64_t x0 = share_begin(tiles_line, cta), x1 = share_begin(tiles_line, cta + 1);
@@ -728,19 +728,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma::mbar_arrive(smem_u32(&sh.desc_full[di]));
         }
       }
-      if (!go) {  // copies in flight must land before the shared memory goes away
-        for (uint32_t i = 0; i < min(filled, (uint32_t)C::STAGES); ++i) {
-          const uint32_t use = filled - 1 - i;
-          const unsigned long long t0 = global_ns();
-          while (!umma::mbar_try_wait(smem_u32(&sh.kv_full[use % C::STAGES]),
-                                      (use / C::STAGES) & 1) &&
-                 global_ns() - t0 < kWaitNs) {
-          }
-        }
+      // Copies in flight must land before the shared memory goes away, also where it is another
+      // warp that gives up, later than this one is done.
+      for (uint32_t i = 0; i < min(filled, (uint32_t)C::STAGES); ++i) {
+        const uint32_t use = filled - 1 - i;
         const unsigned long long t0 = global_ns();
-        while (n_item > 0 && !umma::mbar_try_wait(smem_u32(&sh.q_full), (n_item - 1) & 1) &&
+        while (!umma::mbar_try_wait(smem_u32(&sh.kv_full[use % C::STAGES]),
+                                    (use / C::STAGES) & 1) &&
                global_ns() - t0 < kWaitNs) {
         }
+      }
+      const unsigned long long t0 = global_ns();
+      while (n_item > 0 && !umma::mbar_try_wait(smem_u32(&sh.q_full), (n_item - 1) & 1) &&
+             global_ns() - t0 < kWaitNs) {
       }
     } else if (warp == kMmaWarp) {
       // ---- products ----------------------------------------------------------------------------
@@ -815,7 +815,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!go) break;
         ++n_item;
       }
-      if (!go) {  // let what was issued finish
+      // what was issued finishes before the tensor memory goes away
+      if (n_tile > 0) {
         umma::commit(smem_u32(&sh.drain));
         const unsigned long long t0 = global_ns();
         while (!umma::mbar_try_wait(smem_u32(&sh.drain), 0) && global_ns() - t0 < kWaitNs) {

@@ -74,3 +74,24 @@ def test_every_arrival_for_the_product_warp_stands_behind_the_tensor_memory_fenc
         # the last thing that is not an arrival, a lane's guard or a warp barrier
         block = re.sub(r"(umma::mbar_arrive\([^;]*;|if \(lane == 0\) ?\{?|__syncwarp\(\);|\s)+$", "", before)
         assert block.endswith("umma::fence_before_sync();"), block[-120:]
+
+
+def test_copies_and_products_in_flight_are_waited_for_whoever_gives_up():
+    """The loading and the product warp may be done issuing when another warp gives up: what is in
+    flight lands before the block's shared and tensor memory go, not only if they gave up themselves."""
+    body = between(source(), "if (warp == kLoadWarp) {", "regs_more<kRegsSoftmax>")
+    for wait_for in (r"min\(filled, \(uint32_t\)C::STAGES\)", r"sh\.q_full\), \(n_item - 1\) & 1",
+                     r"umma::commit\(smem_u32\(&sh\.drain\)\)"):
+        (at,) = [m.start() for m in re.finditer(wait_for, body)]
+        # the open blocks around it: none of them is a condition on this warp's own giving up
+        depth, i, opened = 0, at, []
+        while i > 0:
+            i -= 1
+            if body[i] == "}":
+                depth += 1
+            elif body[i] == "{":
+                if depth:
+                    depth -= 1
+                else:
+                    opened.append(body[body.rfind("\n", 0, i) + 1:i].strip())
+        assert opened and not any(re.search(r"\bgo\b", o) for o in opened), opened
