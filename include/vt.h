@@ -325,8 +325,8 @@ vt_status vt_plan_requests(const int32_t* seq_lens, int32_t batch, int32_t* orde
  * over the request's other pages, zero with lse = -inf where none is left.  Pool slots behind
  * a request's last token are never used, whatever they hold; K and V of the tokens a request
  * has, and the scaled scores, must be finite (a query row that is not spoils its own results
- * only).  out and lse may not overlap the inputs.  Scores, softmax statistics and accumulators are fp32; the weights are
- * rounded once to bf16 for their product with V.
+ * only).  out and lse may not overlap the inputs.  Scores, softmax statistics and accumulators
+ * are fp32; the weights are rounded once to bf16 for their product with V.
  * Head shapes: (64, 64) and (128, 128), Hq/Hkv <= 8.  Pool strides as everywhere, and not 0
  * for a dimension of more than one entry.
  */
@@ -478,7 +478,8 @@ vt_status vt_free_requests(const vt_page_books* books, int64_t num_pages, const 
  * with an id >= u moves to the k-th lowest free id < u.  Contents, centroid rows (fp32
  * [P, Hkv, D] or NULL), refs and the live entries of page_table follow; n_used[0] = u.  Bad
  * page ids in the table stay (VT_DEV_BAD_PAGE), and so do live entries whose page has no
- * reference (VT_DEV_BAD_REF).  workspace: vt_page_workspace_size(num_pages, 0).
+ * reference (VT_DEV_BAD_REF): that page counts as free, so a page that moves may be copied over
+ * it.  workspace: vt_page_workspace_size(num_pages, 0).
  */
 vt_status vt_compact_pages(const vt_paged_kv* kv, const vt_page_books* books, float* centroids,
                            int32_t* n_used, void* workspace, size_t workspace_bytes,

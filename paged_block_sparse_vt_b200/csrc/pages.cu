@@ -407,8 +407,8 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kScanThreads, 1)
     for (int e = 0; e < 4; ++e) {
       const int64_t id = x + e;
       if (id < sh.hi) {
+        p.move_of[id] = !f[e] ? -1 : id < u ? 0 : k - used_u;
         if (id >= u) {
-          p.move_of[id] = f[e] ? k - used_u : -1;
           if (f[e]) p.src[k - used_u] = (int)id;
         } else if (!f[e]) {
           p.dst[id - k] = (int)id;
@@ -447,10 +447,10 @@ __global__ void __launch_bounds__(kCopyThreads)
       const int page = t[k];
       if (page < 0 || page >= p.num_pages) {
         flag(p.status, VT_DEV_BAD_PAGE);
-      } else if (page >= u) {
+      } else {  // (the counts change meanwhile; what the plan noted of them does not)
         const int m = p.move_of[page];
-        if (m >= 0) t[k] = p.dst[m];
-        else flag(p.status, VT_DEV_BAD_REF);
+        if (m < 0) flag(p.status, VT_DEV_BAD_REF);
+        else if (page >= u) t[k] = p.dst[m];
       }
     }
   }

@@ -57,7 +57,7 @@ struct CompactParams {
   int32_t* n_moves;  // workspace: one word, then num_pages words each
   int32_t* src;      //   the page of move m
   int32_t* dst;      //   where it goes
-  int32_t* move_of;  //   the move of a page at or above n_used, -1 none
+  int32_t* move_of;  //   -1 for a free page; the move of a used one at or above n_used, else 0
 };
 
 cudaError_t launch_copy_pages(const PagePools& pools, const int32_t* src, const int32_t* dst, int n,
