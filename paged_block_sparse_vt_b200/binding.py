@@ -436,7 +436,8 @@ def vt_plan_requests(seq_lens: torch.Tensor, order: Optional[torch.Tensor] = Non
 # These run once per layer and step, often on little work, so their checks are written flat: one
 # test per tensor, and the words for a failure only when there is one.
 
-_current_device = torch._C._cuda_getDevice
+# (a torch built without CUDA has neither this nor the raw stream above; the package imports there)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _devices = [torch.device("cuda", i) for i in range(64)]
 
 
