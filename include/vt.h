@@ -412,9 +412,10 @@ size_t vt_shared_prefix_workspace_size(const vt_paged_kv* kv, const vt_shared_pr
  * copied, on the device; nothing is read back.  Pages are always taken lowest free id first,
  * in the order of the list, so results do not depend on timing.  Calls on the same books must
  * be ordered (one stream, or events).  Lists are int32 device arrays; entries outside [0, R)
- * are skipped (VT_DEV_BAD_REQ).  Page copies move the K rows, the V rows (unless v_pool ==
- * k_pool) and, where a centroid cache is given, the centroid rows.  All head shapes that
- * vt_build_centroids takes, the MLA latent form (one copy of the shared rows) among them.
+ * are skipped (VT_DEV_BAD_REQ).  Page copies move the K rows, the V rows (unless they lie within
+ * the K rows: the same pool and strides, and no more dims) and, where a centroid cache is given,
+ * the centroid rows.  All head shapes that vt_build_centroids takes, the MLA latent form (one copy
+ * of the shared rows) among them.
  */
 typedef struct {
   int32_t rows; /* R */

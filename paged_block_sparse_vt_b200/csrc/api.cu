@@ -439,7 +439,7 @@ vt_status check_books(const vt_page_books* b, int64_t num_pages, int64_t* entrie
   return ok();
 }
 
-// The pools as byte-for-byte copies see them; *sides: 1 where V is the K rows.
+// The pools as byte-for-byte copies see them; *sides: 1 where the V rows lie within the K rows.
 vt_status page_pools(const vt_paged_kv* kv, float* centroids, PagePools* p, int* sides) {
   vt_status s = check_kv(kv);
   if (s != VT_OK) return s;
@@ -456,7 +456,10 @@ vt_status page_pools(const vt_paged_kv* kv, float* centroids, PagePools* p, int*
   p->num_pages = kv->num_pages;
   p->centroids = centroids;
   p->cent_row = (int64_t)kv->num_kv_heads * kv->head_dim;
-  *sides = kv->k_pool == kv->v_pool ? 1 : 2;
+  *sides = kv->k_pool == kv->v_pool && kv->head_dim_v <= kv->head_dim && kv->sk_p == kv->sv_p &&
+                   kv->sk_t == kv->sv_t && kv->sk_h == kv->sv_h
+               ? 1
+               : 2;
   return ok();
 }
 
