@@ -554,6 +554,12 @@ def _workspace(workspace, need: int, dev: int):
     return workspace, _vec(workspace, "workspace", torch.uint8, dev), workspace.numel()
 
 
+# What the C side decides by sizes and the binding relies on, so as not to ask at every call (held
+# together by tests/test_workspace_rules.py): lists of up to LIST_SMEM rows grow without a
+# workspace; prompts of PREFILL_SAME_WS tokens or more all need the same one.
+LIST_SMEM = 2048
+PREFILL_SAME_WS = 1024
+
 # Bytes of workspace by what they depend on beside the device: a few shapes in a program's life.
 _ws_bytes: dict = {}
 
@@ -582,7 +588,7 @@ def _device_call(fn, where: str, dev: int, *args) -> None:
 
 
 def _prefill_ws(lib, dev: int, kv: PagedKV, a: PrefillArgs) -> int:
-    if a.num_tokens < 1024:  # (small calls need none; larger ones the same, whatever their sizes)
+    if a.num_tokens < PREFILL_SAME_WS:
         return int(_on_device(dev, lib.vt_prefill_workspace_size, kv, a))
     return _ws_size(("prefill", dev, kv.head_dim),
                     lambda: _on_device(dev, lib.vt_prefill_workspace_size, kv, a))
@@ -750,7 +756,7 @@ def vt_extend_requests(page_table, seq_lens, refs, requests, tokens, status=None
     n, a, b = _lists(dev, requests, tokens, ("requests", "tokens"))
     pages = refs.numel()
     ws, ws_bytes = None, 0
-    if n > 2048:  # (shorter lists use none)
+    if n > LIST_SMEM:
         workspace, ws, ws_bytes = _page_ws(lib, workspace, pages, n, dev)
     _device_call(lib.vt_extend_requests, "vt_extend_requests", dev, books, pages, a, b, n, ws,
                  ws_bytes)
