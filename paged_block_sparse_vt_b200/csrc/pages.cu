@@ -23,11 +23,14 @@ namespace vt {
 namespace {
 
 constexpr int kScanCtas = 8;
-// A pool of up to this many pages is scanned by one CTA: four reads each of its threads, against
-// a cluster's launch and two barriers of eight.
-constexpr int64_t kOneCta = 16384;
 constexpr int kScanThreads = 1024;
 constexpr int kScanTile = kScanThreads * 4;  // counts per step: an int4 each
+// A pool of up to this many pages is scanned by one CTA: one step of its threads, against a
+// cluster's launch and barriers of eight CTAs.  One CTA and a cluster, in a chain of calls: a
+// compaction in which nothing moves 7.4 and 8.4 us (500 pages), 8.8 and 9.8 (4096), 11.5 and 9.9
+// (8192), 14.0 and 10.1 (12000), 21.9 and 10.2 (24000); a growth of 4 rows 9.1 and 9.4 (4096), 9.6
+// and 9.8 (8192), 10.3 and 9.8 (12000), 10.7 and 9.6 (24000).
+constexpr int64_t kOneCta = kScanTile;
 
 // Page count of `len` tokens (len >= 0, also close to 2^31).
 __device__ __forceinline__ int pages_of(int len) { return len / kPage + (len % kPage != 0); }
