@@ -1305,7 +1305,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // not, no item is cut, and there is nothing to join and no workspace.
 bool may_split(const AttendParams& p) {
   const int64_t tpt = kTile / p.G, items = p.Hkv * (p.T / (2 * tpt) + std::min<int64_t>(p.B, p.T));
-  return items * kCostTwo * (kCostItem + p.max_pages * kPage) >= 2 * kMinShare;
+  return items * kCostKey * (kCostItem + p.max_pages * kPage) >= 2 * kMinShare;
 }
 
 // Fills w from ws (NULL: only the size is wanted) and returns the bytes.

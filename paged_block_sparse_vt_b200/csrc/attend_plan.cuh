@@ -20,21 +20,27 @@ namespace vt {
 constexpr int kTile = 128;  // query rows of one accumulator tile; an item has two
 constexpr int kKeys = 128;  // keys of one step
 
-// Costs, in keys times a weight.  An item of one row tile takes as long as one of two: nothing
-// runs beside its chain of scores, softmax and values (a step of 128 keys: 3.7 k cycles, and of
-// two row tiles 3.5 k).
-constexpr int kCostTwo = 4, kCostOne = 4;
-constexpr int kCostItem = 256;      // loading q, filling the pipeline, writing out
-constexpr int64_t kMinShare = 4 * kKeys * kCostTwo;  // no CTA takes less than four key tiles
+// Costs, in keys times what a key costs, which is the same for an item of one row tile and one of
+// two.  A step of 128 keys takes ~3200 cycles with two and 2400-2900 with one, by a fit over whole
+// calls: nothing runs beside the chain of a single tile.  Yet shares cut with 3/4 of the cost for
+// one tile are the slower ones (387 us with equal costs, 393 so for the packed prompts, 908 and 934
+// for the chunks, 193 and 201 for the prefix groups, 519 and 553 for the document; cold inputs).
+constexpr int kCostKey = 4;
+constexpr int kCostItem = 256;      // loading q, filling the pipeline, writing out: two steps
+constexpr int64_t kMinShare = 4 * kKeys * kCostKey;  // no CTA takes less than four key tiles
 
 // The second line: pages of a request's own, for each KV head, and what an item of them costs
 // beyond (its query, its result).
 constexpr int kWarps = 12;        // of a CTA, each with a share
 constexpr int kOwnItem = 2;       // pages
 constexpr int kMinPages = 4;      // no warp takes less
-// A page of one head in the costs of the first line, measured: 256 requests on one prefix of 65536
-// tokens took 791 us with 20, 639 with 35, 565 with 50, 552 with 70; 128 requests with long own
-// parts 176, 184, 185, 215.
+// A page of one head in the costs of the first line: one value for every shape.  Measured (us, cold
+// inputs) with 20 / 30 / 45 / 60 / 80, at 128 dims: 128 requests on five prefixes of 12800 tokens
+// with 100-4096 own, 32/8 heads 223 / 207 / 221 / 248 / 291; 256 on one of 65536 with 17-300 own,
+// 32/8 heads 406 / 306 / 315 / 315 / 315, 48/8 heads 604 / 512 / 459 / 494 / 495, 64/8 heads
+// 834 / 603 / 585 / 575 / 588.  At 64 dims, where a step costs nearly as much and a page half, the
+// best is lower: the five prefixes 141 / 156 / 180 / 208 / 248 (32/8 heads), the document
+// 403 / 408 / 410 / 420 / 426 (48/8).
 constexpr int kOwnPage = 45;
 
 struct Unit {
@@ -63,9 +69,8 @@ VT_HD int item_keys(const Unit& u, int tpt, int t) {
   return u.vis0 + (last < u.n ? last : u.n) - 1;
 }
 
-VT_HD int item_weight(const Unit& u, int tpt, int t) {
-  return u.n - t * 2 * tpt > tpt ? kCostTwo : kCostOne;
-}
+// What a key costs in item t.
+VT_HD int item_weight(const Unit&, int, int) { return kCostKey; }
 
 VT_HD int64_t item_cost(const Unit& u, int tpt, int t) {
   return (int64_t)item_weight(u, tpt, t) * (kCostItem + item_keys(u, tpt, t));
@@ -78,7 +83,7 @@ VT_HD int64_t cost_before(const Unit& u, int tpt, int t) {
   const int64_t f = t < n ? t : n - 1;
   int64_t keys = f * u.vis0;
   if (u.step) keys += 2 * (int64_t)tpt * (f * (f + 1) / 2) - f;
-  const int64_t c = kCostTwo * (f * kCostItem + keys);
+  const int64_t c = kCostKey * (f * kCostItem + keys);
   return t < n ? c : c + item_cost(u, tpt, n - 1);
 }
 
