@@ -408,14 +408,14 @@ size_t vt_shared_prefix_workspace_size(const vt_paged_kv* kv, const vt_shared_pr
  * The cache's books are three int32 device arrays of the caller: page_table, R rows of max_pages
  * entries that stand pt_stride apart (1 <= max_pages <= pt_stride, 0 means pt_stride; what is
  * between the rows is neither read nor written), seq_lens [R] (0: the row holds no request) and
- * refs [num_pages], the number of rows that use a page (0: free).  The calls below change the books, and the pools where pages are
- * copied, on the device; nothing is read back.  Pages are always taken lowest free id first,
- * in the order of the list, so results do not depend on timing.  Calls on the same books must
- * be ordered (one stream, or events).  Lists are int32 device arrays; entries outside [0, R)
- * are skipped (VT_DEV_BAD_REQ).  Page copies move the K rows, the V rows (unless they lie within
- * the K rows: the same pool and strides, and no more dims) and, where a centroid cache is given,
- * the centroid rows.  All head shapes that vt_build_centroids takes, the MLA latent form (one copy
- * of the shared rows) among them.
+ * refs [num_pages], the number of rows that use a page (0: free).  The calls below change the
+ * books, and the pools where pages are copied, on the device; nothing is read back.  Pages are
+ * always taken lowest free id first, in the order of the list, so results do not depend on
+ * timing.  Calls on the same books must be ordered (one stream, or events).  Lists are int32
+ * device arrays; entries outside [0, R) are skipped (VT_DEV_BAD_REQ).  Page copies move the K
+ * rows, the V rows (unless they lie within the K rows: the same pool and strides, and no more
+ * dims) and, where a centroid cache is given, the centroid rows.  All head shapes that
+ * vt_build_centroids takes, the MLA latent form (one copy of the shared rows) among them.
  */
 typedef struct {
   int32_t rows; /* R */

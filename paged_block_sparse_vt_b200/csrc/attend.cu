@@ -11,6 +11,10 @@
 //   p_j = 2^(c S_t[r, j] - ref), l = l + sum_j p_j      with c = scale log2 e
 //   P_t = bf16(p)                (over the columns of S_t)
 //   O_t = O_t + P_t V            (tcgen05, P_t read from tensor memory)
+// The weights are rounded to bf16 because the tensor core wants P in V's type (one 16-bit kind for
+// both operands; the 32-bit kind has half the rate and would need V widened on the way): half a
+// step, 2^-8, of each weight at most, which brings the results' rms error from the output's own
+// rounding, 0.0016-0.0017 of their size, to 0.0017-0.0022.  l sums the weights as they were before.
 // A warpgroup has one tile, a thread one row, so no sum crosses lanes.  The reference need not be
 // the largest score: out = O / l does not depend on it, and a weight of 2^50 keeps as many bits in
 // bf16 and fp32 as one of 1.  So a step takes no maximum.  Its reference is that of the first
@@ -53,8 +57,9 @@ namespace {
 
 // two softmax warpgroups, and one with the loading and the product warp
 constexpr int kThreads = 384;
-// Registers: a softmax thread holds its row of scores, 128 of them, beside the rest; what the
-// third warpgroup gives up goes to the other two (2 * 200 + 104 = 3 * 168, the launch's share).
+// Registers: a softmax thread holds 64 scores of its row (32 in flight behind 32 in use) and 32
+// pairs of weights beside the rest; what the third warpgroup gives up goes to the other two
+// (2 * 200 + 104 = 3 * 168, the launch's share).
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kDescs = 4;       // items described ahead
@@ -320,10 +325,13 @@ struct OwnCursor {
 };
 
 // One warp's share [x0, x1) of the second line: the pages one after the other, two of them in
-// flight in its two slots of shared memory, across items too.  Bound by what is in flight: twelve
-// warps with 2 x 8 KB each (128 dims) read 64 requests of 4096 tokens at 5.2 TB/s of the 6.5 a copy
-// reaches.  (Decode rows as tcgen05 items, with six 32 KB stages in flight: the same rate for long
-// rows, and ~9000 cycles for one of two key tiles, three times what the warps take.)
+// flight in its two slots of shared memory, across items too.  64 requests of 4096 tokens (128
+// dims) are read at 5.6 TB/s (193 us) of the 6.5 a copy reaches.  Memory is not what bounds it: 200
+// KB in flight per SM are more than it needs, and a warp waits for it in 28% of its time only.  It
+// is each warp's own chain per page - products, softmax, products, refill of the slot just used -
+// of which three warps on a scheduler issue in 47% of the cycles (ncu).  (Decode rows as tcgen05
+// items, with six 32 KB stages in flight: the same rate for long rows, and ~9000 cycles for one of
+// two key tiles, three times what the warps take.)
 template <int D>
 __device__ __forceinline__ void own_share(const AttendParams& p, const Work& w, OwnCursor cur,
                                           int64_t x0, int64_t x1, uint32_t smem, int ws, int lane) {
@@ -1157,7 +1165,7 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = kJoinThreads / 32;
 
 // Prompts: block (c, y) joins rows y * 8 .. of the item that begins in CTA c and ends in another.
-// At most one item per CTA, two or three pieces each, out of L2: 6-12 us behind a large batch.
+// At most one item per CTA, two or three pieces each, out of L2: ~10 us behind a packed batch.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
     join_items_kernel(const AttendParams p, const Work w) {
@@ -1183,7 +1191,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 // Shared prefixes: a warp joins one row, the pieces of its group's prefix and of its own pages.
-// The time is a chain of trips to memory (10 us for 32 samples of a prompt), so it has few links:
+// The time is a chain of trips to memory (11 us by itself for 32 samples of a prompt, a quarter of
+// the call), so it has few links:
 // which shares hold a piece is worked out a lane each, all their m and l are read at once, and the
 // rows eight at a time.
 template <int D>

@@ -140,7 +140,8 @@ namespace vt {
 
 // ---- a second launch that follows its first closely ----------------------------------------
 // The first kernel lets the second be set up while it still runs; the second waits for its end
-// (and its writes) before it reads anything.
+// before it reads anything that the first writes.  (Inputs of both it may read before: the first
+// is launched the usual way, behind the end of whatever wrote them.)
 __device__ __forceinline__ void let_next_launch() {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }

@@ -48,8 +48,7 @@ def test_a_bounded_wait_has_one_answer_for_the_warp():
     assert polls and all(x == "(__all_sync(kFull, " or x.endswith("__all_sync(kFull, ")
                          for x in polls), polls
     gives_up = between(body, "while (", "return false")
-    assert re.search(r"if \(__any_sync\(kFull, \*abort_flag != 0 \|\| global_ns\(\) - t0 > kWaitNs\)\)",
-                     gives_up)
+    assert "if (__any_sync(kFull, *abort_flag != 0 || global_ns() - t0 > kWaitNs))" in gives_up
     assert body.count("return false") == 1
     # nothing that calls it stands in a lane's own block
     for m in re.finditer(r"\bwait\(smem_u32", text):
@@ -72,13 +71,14 @@ def test_every_arrival_for_the_product_warp_stands_behind_the_tensor_memory_fenc
     for at in arrivals:
         before = text[:at]
         # the last thing that is not an arrival, a lane's guard or a warp barrier
-        block = re.sub(r"(umma::mbar_arrive\([^;]*;|if \(lane == 0\) ?\{?|__syncwarp\(\);|\s)+$", "", before)
+        block = re.sub(r"(umma::mbar_arrive\([^;]*;|if \(lane == 0\) ?\{?|__syncwarp\(\);|\s)+$", "",
+                       before)
         assert block.endswith("umma::fence_before_sync();"), block[-120:]
 
 
 def test_copies_and_products_in_flight_are_waited_for_whoever_gives_up():
     """The loading and the product warp may be done issuing when another warp gives up: what is in
-    flight lands before the block's shared and tensor memory go, not only if they gave up themselves."""
+    flight lands before the block's shared and tensor memory go, whoever gave up."""
     body = between(source(), "if (warp == kLoadWarp) {", "regs_more<kRegsSoftmax>")
     for wait_for in (r"min\(filled, \(uint32_t\)C::STAGES\)", r"sh\.q_full\), \(n_item - 1\) & 1",
                      r"umma::commit\(smem_u32\(&sh\.drain\)\)"):
