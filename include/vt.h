@@ -324,8 +324,9 @@ vt_status vt_plan_requests(const int32_t* seq_lens, int32_t batch, int32_t* orde
  * page id outside [0, num_pages) takes no part (VT_DEV_BAD_PAGE): the rows are the attention
  * over the request's other pages, zero with lse = -inf where none is left.  Pool slots behind
  * a request's last token are never used, whatever they hold; K and V of the tokens a request
- * has, and the scaled scores, must be finite (a query row that is not spoils its own results
- * only).  out and lse may not overlap the inputs.  Scores, softmax statistics and accumulators
+ * has, and the scaled scores, must be finite, and |V| below 2^80 (weights of up to 2^40 are summed
+ * before they are scaled down); a query row that is not finite spoils its own results only.
+ * out and lse may not overlap the inputs.  Scores, softmax statistics and accumulators
  * are fp32; the weights are rounded once to bf16 for their product with V.
  * Head shapes: (64, 64) and (128, 128), Hq/Hkv <= 8.  Pool strides as everywhere, and not 0
  * for a dimension of more than one entry.
